@@ -320,6 +320,168 @@ cg_status cg_decode_attention(const cg_kv_desc* kv, const cg_codec_desc* codec, 
                               const void* zeros_dev, const float* G_dev, float* out_dev, void* workspace_dev,
                               uint64_t workspace_bytes, void* stream);
 
+/* ---- 8-bit KV cache with a scale for each block of tokens and head ----------------------
+ *
+ * A cache that takes tokens one at a time, at a position of its own for every
+ * sequence, and is read by attention as it is (deployment entry points of the
+ * library; the paper's own codec is cg_encode).  Buffers, for a cg_kv_desc
+ * {L, B, H, T, d} and blocks of tb tokens:
+ *   codes   [L][2][B][H][T][d]       one byte a value, int8 or e4m3 (s = 0 keys, 1 values)
+ *   scales  fp32 [L][2][B][H][T/tb]  powers of two; code c of a block stands for s c
+ *   bounds  int8 [L][B][H][T/tb][2][d]  the least [0] and largest [1] key code of every
+ *           channel of a block (e4m3: in units of 448 / 127, rounded outwards), which
+ *           cg_cache8_select reads; optional
+ *   mass    fp32 [L][B][H][T/tb]     the attention weight a block has drawn, which
+ *           cg_cache8_evict reads; optional
+ * Lengths and positions are device int32 [B], read when the kernels run (a captured
+ * call follows them); none of them can make a call reach outside its buffers: a
+ * length counts as clamped to [0, max_tokens], and what lies beyond is not read.
+ * Nothing needs clearing before use except `mass`.  Every call works on the layers
+ * [layer0, layer0 + n_layers) of the cache; its inputs and outputs other than the
+ * cache hold only those.  Requests whose grid would pass 2^31 - 1 blocks return
+ * CG_ERR_TOO_LARGE.  Results do not depend on timing (no floating-point atomics). */
+typedef enum {
+  CG_CACHE8_INT8 = 0, /* codes -127 .. 127 */
+  CG_CACHE8_E4M3 = 1  /* codes -448 .. 448, four bits of exponent and three of mantissa */
+} cg_cache8_code;
+
+/* code: cg_cache8_code.  tb: tokens of a block, 16, 32 or 64; T is a multiple of it. */
+typedef struct {
+  int32_t code;
+  int32_t tb;
+} cg_cache8_desc;
+
+/* Sizes of the four buffers: bytes of codes and bounds, fp32 entries of scales and mass. */
+typedef struct {
+  uint64_t code_bytes;
+  uint64_t scale_count;
+  uint64_t bound_bytes;
+  uint64_t mass_count;
+} cg_cache8_sizes;
+
+/* Host only. */
+cg_status cg_cache8_sizes_for(const cg_kv_desc* kv, const cg_cache8_desc* c8, cg_cache8_sizes* out);
+
+/* Appends tokens: token j of sequence b goes to position pos[b] + j, j < counts[b].
+ *   new_dev     bf16 [n_layers][2][B][H][n_new][d] (input)
+ *   pos_dev     int32 [B]: tokens the sequence holds already
+ *   counts_dev  int32 [B], how many of the n_new tokens each sequence takes (clamped to
+ *               [0, n_new]), or NULL: all
+ *   codes_dev, scales_dev, bounds_dev  the cache (bounds may be NULL)
+ * A block's scale is the least power of two s >= 2^-126 with |x| <= top s for what it
+ * holds (top = 127 or 448), and c = rnd(x / s), ties to even.  A block that already
+ * holds tokens keeps its scale unless a new one needs a larger: then its older codes
+ * are rounded anew, c = rnd(c s_old / s), and its bounds formed anew; else the bounds
+ * are widened.  (A scale that is no positive finite number marks a block without tokens.) Positions at and behind the last new token are left as they are, and
+ * tokens whose position is outside [0, T) are not stored (a sequence with a negative
+ * pos stores none). */
+cg_status cg_cache8_append(const cg_kv_desc* kv, const cg_cache8_desc* c8, int32_t layer0, int32_t n_layers, int32_t n_new,
+                           const void* new_dev, const int32_t* pos_dev, const int32_t* counts_dev, uint8_t* codes_dev,
+                           float* scales_dev, int8_t* bounds_dev, void* stream);
+
+/* Attention of the newest tokens over the cache.
+ *   q_heads     Hq, a multiple of H with Hq / H <= 16; query head j uses KV head j / (Hq / H)
+ *   q_tokens    query tokens of every sequence, 1 .. 16: token i is the cached position
+ *               p_i = len - q_tokens + i and sees the positions 0 .. p_i
+ *   max_tokens  no length of the batch is above it (it sizes the work and the workspace)
+ *   n_select    0: every position is read; else that many listed blocks are (sel_dev)
+ *   accumulate  mass_dev: 0 sets it, 1 adds to it
+ *   scale       score scale, usually 1 / sqrt(d_head) */
+typedef struct {
+  int32_t q_heads;
+  int32_t q_tokens;
+  int32_t layer0;
+  int32_t n_layers;
+  int32_t max_tokens;
+  int32_t n_select;
+  int32_t accumulate;
+  float scale;
+} cg_cache8_attn_desc;
+
+/* Workspace bytes of cg_cache8_attention, with or without mass_dev (host only). */
+cg_status cg_cache8_attention_workspace_size(const cg_kv_desc* kv, const cg_cache8_desc* c8, const cg_cache8_attn_desc* at,
+                                             int32_t want_mass, uint64_t* bytes);
+
+/* out = sum_t softmax_t(scale q . k_t) v_t over the positions that each query token sees
+ * (a query token that sees none gives zeros).
+ *   q_dev     bf16 [n_layers][B][Hq][q_tokens][d] (input)
+ *   lens_dev  int32 [B], the query tokens' own positions included
+ *   sel_dev   int32 [n_layers][B][H][q_tokens][n_select], blocks of each KV head and query
+ *             token, as cg_cache8_select writes them: any order; entries outside the blocks
+ *             that the token sees (-1 for one) count nothing, an entry given twice counts
+ *             twice.  NULL exactly if n_select = 0
+ *   out_dev   fp32 [n_layers][B][Hq][q_tokens][d] (output)
+ *   mass_dev  NULL, or the whole cache's mass: for the call's layers, the softmax weight of
+ *             every block summed over the query heads of its KV head and the query tokens
+ *             is set (0 for blocks behind the length) or, with accumulate, added to the
+ *             blocks that the sequence has.  Only with n_select = 0 (else
+ *             CG_ERR_UNSUPPORTED)
+ *   workspace_dev / workspace_bytes: at least cg_cache8_attention_workspace_size(); nothing
+ *             in it outlives the call
+ * Scores, maxima and sums are fp32; the softmax weights enter the product with the values
+ * as two fp16 terms (2^-22).  Scales have to be powers of two, as cg_cache8_append
+ * writes them. */
+cg_status cg_cache8_attention(const cg_kv_desc* kv, const cg_cache8_desc* c8, const cg_cache8_attn_desc* at,
+                              const void* q_dev, const uint8_t* codes_dev, const float* scales_dev, const int32_t* lens_dev,
+                              const int32_t* sel_dev, float* out_dev, float* mass_dev, void* workspace_dev,
+                              uint64_t workspace_bytes, void* stream);
+
+/* Block selection: the first fields as in cg_cache8_attn_desc; n_select blocks for each KV
+ * head and query token, among them the first sink_blocks and the last recent_blocks of
+ * those it sees (sink_blocks + recent_blocks <= n_select <= T / tb). */
+typedef struct {
+  int32_t q_heads;
+  int32_t q_tokens;
+  int32_t layer0;
+  int32_t n_layers;
+  int32_t max_tokens;
+  int32_t n_select;
+  int32_t sink_blocks;
+  int32_t recent_blocks;
+} cg_cache8_select_desc;
+
+/* Workspace bytes of cg_cache8_select (host only). */
+cg_status cg_cache8_select_workspace_size(const cg_kv_desc* kv, const cg_cache8_desc* c8, const cg_cache8_select_desc* sd,
+                                          uint64_t* bytes);
+
+/* Chooses for each KV head and query token the blocks whose bounds promise the largest
+ * scores.  With q8 = rnd(q / 2^e) a query row in whole numbers, e the least with
+ * |q| <= 127 2^e, a block's score is
+ *   max over the KV head's query heads of  2^e s_K sum_c max(q8_c lo_c, q8_c hi_c),
+ * exact in fp32; ties go to the lowest block.
+ *   q_dev, scales_dev, bounds_dev, lens_dev  as above (input)
+ *   sel_dev  int32 [n_layers][B][H][q_tokens][n_select] (output): block indices, ascending,
+ *            then -1 where the token sees fewer than n_select blocks */
+cg_status cg_cache8_select(const cg_kv_desc* kv, const cg_cache8_desc* c8, const cg_cache8_select_desc* sd, const void* q_dev,
+                           const float* scales_dev, const int8_t* bounds_dev, const int32_t* lens_dev, int32_t* sel_dev,
+                           void* workspace_dev, uint64_t workspace_bytes, void* stream);
+
+/* Eviction: of the ceil(len / tb) blocks of a sequence, at most keep_blocks stay: the first
+ * sink_blocks, the last recent_blocks (>= 1: the last block may be partly filled) and of the
+ * others those with the largest mass. */
+typedef struct {
+  int32_t layer0;
+  int32_t n_layers;
+  int32_t keep_blocks;
+  int32_t sink_blocks;
+  int32_t recent_blocks;
+} cg_cache8_evict_desc;
+
+/* Moves the blocks that stay, in their order and as they are (codes, scales, bounds, mass),
+ * to the front of another cache with the same layers, batch, heads and d_head and a capacity
+ * of its own.  Every (layer, KV head) keeps blocks of its own choice; all keep the same number.
+ *   lens_dev  int32 [B];  mass_dev: ties go to the lowest block, NaN counts as lowest
+ *   bounds_dev, to_bounds_dev  both or neither NULL
+ *   to_mass_dev  the kept blocks' mass, then 0 up to the capacity
+ *   to_lens_dev  int32 [B]: len, or len - tb (blocks - keep_blocks) where blocks went
+ *   kept_dev     int32 [n_layers][B][H][keep_blocks]: the blocks that stayed, then -1
+ * What lies behind the kept blocks of the other cache is left as it is (except mass).  The
+ * two caches may not overlap (CG_ERR_INVALID). */
+cg_status cg_cache8_evict(const cg_kv_desc* kv, const cg_cache8_desc* c8, const cg_cache8_evict_desc* ev, const int32_t* lens_dev,
+                          const uint8_t* codes_dev, const float* scales_dev, const int8_t* bounds_dev, const float* mass_dev,
+                          const cg_kv_desc* to_kv, uint8_t* to_codes_dev, float* to_scales_dev, int8_t* to_bounds_dev,
+                          float* to_mass_dev, int32_t* to_lens_dev, int32_t* kept_dev, void* stream);
+
 /* Workspace bytes cg_spectral_stats needs for this shape (host only). */
 cg_status cg_spectral_workspace_size(const cg_kv_desc* kv, const cg_stats_desc* st,
                                      int32_t want_grad, uint64_t* bytes);

@@ -17,12 +17,14 @@ LIB_PATH = os.path.join(_PKG, "libcg.so")
 CG_OK, CG_ERR_INVALID, CG_ERR_UNSUPPORTED, CG_ERR_CUDA, CG_ERR_TIMEOUT, CG_ERR_TOO_LARGE, CG_ERR_BOUND = range(7)
 BLOCK_UNIFORM, KIVI = 0, 1
 ENGINE_AUTO, ENGINE_CUDA_CORES, ENGINE_CHAIN_TENSOR = 0, 1, 2
+CACHE8_INT8, CACHE8_E4M3 = 0, 1
 
 # Every symbol include/cg.h declares.
 EXPORTS = ("cg_sizes_for", "cg_gauge_build", "cg_gauge_grad", "cg_adamw_step", "cg_group_gram", "cg_encode",
            "cg_decode", "cg_roundtrip_workspace_size", "cg_roundtrip_host", "cg_decode_attention_workspace_size",
-           "cg_decode_attention", "cg_spectral_workspace_size",
-           "cg_spectral_stats", "cg_spectral_stats_noalloc", "cg_selftest_wait_timeout", "cg_sync_status",
+           "cg_decode_attention", "cg_cache8_sizes_for", "cg_cache8_append", "cg_cache8_attention_workspace_size",
+           "cg_cache8_attention", "cg_cache8_select_workspace_size", "cg_cache8_select", "cg_cache8_evict",
+           "cg_spectral_workspace_size", "cg_spectral_stats", "cg_spectral_stats_noalloc", "cg_selftest_wait_timeout", "cg_sync_status",
            "cg_last_cuda_error", "cg_status_string", "cg_version")
 
 
@@ -61,6 +63,32 @@ class AttnDesc(ctypes.Structure):
                 ("n_layers", ctypes.c_int32), ("scale", ctypes.c_float)]
 
 
+class Cache8Desc(ctypes.Structure):
+    _fields_ = [("code", ctypes.c_int32), ("tb", ctypes.c_int32)]
+
+
+class Cache8Sizes(ctypes.Structure):
+    _fields_ = [("code_bytes", ctypes.c_uint64), ("scale_count", ctypes.c_uint64), ("bound_bytes", ctypes.c_uint64),
+                ("mass_count", ctypes.c_uint64)]
+
+
+class Cache8AttnDesc(ctypes.Structure):
+    _fields_ = [("q_heads", ctypes.c_int32), ("q_tokens", ctypes.c_int32), ("layer0", ctypes.c_int32),
+                ("n_layers", ctypes.c_int32), ("max_tokens", ctypes.c_int32), ("n_select", ctypes.c_int32),
+                ("accumulate", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class Cache8SelectDesc(ctypes.Structure):
+    _fields_ = [("q_heads", ctypes.c_int32), ("q_tokens", ctypes.c_int32), ("layer0", ctypes.c_int32),
+                ("n_layers", ctypes.c_int32), ("max_tokens", ctypes.c_int32), ("n_select", ctypes.c_int32),
+                ("sink_blocks", ctypes.c_int32), ("recent_blocks", ctypes.c_int32)]
+
+
+class Cache8EvictDesc(ctypes.Structure):
+    _fields_ = [("layer0", ctypes.c_int32), ("n_layers", ctypes.c_int32), ("keep_blocks", ctypes.c_int32),
+                ("sink_blocks", ctypes.c_int32), ("recent_blocks", ctypes.c_int32)]
+
+
 class CgError(RuntimeError):
     def __init__(self, status, where):
         self.status = status
@@ -96,6 +124,17 @@ def lib():
                                                          ctypes.POINTER(u64)]
         L.cg_decode_attention.argtypes = [ctypes.POINTER(KvDesc), ctypes.POINTER(CodecDesc), ctypes.POINTER(AttnDesc),
                                           vp, vp, vp, vp, vp, vp, vp, u64, vp]
+        kvp, c8p = ctypes.POINTER(KvDesc), ctypes.POINTER(Cache8Desc)
+        L.cg_cache8_sizes_for.argtypes = [kvp, c8p, ctypes.POINTER(Cache8Sizes)]
+        L.cg_cache8_append.argtypes = [kvp, c8p, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp]
+        L.cg_cache8_attention_workspace_size.argtypes = [kvp, c8p, ctypes.POINTER(Cache8AttnDesc), i32,
+                                                         ctypes.POINTER(u64)]
+        L.cg_cache8_attention.argtypes = [kvp, c8p, ctypes.POINTER(Cache8AttnDesc), vp, vp, vp, vp, vp, vp, vp, vp, u64,
+                                          vp]
+        L.cg_cache8_select_workspace_size.argtypes = [kvp, c8p, ctypes.POINTER(Cache8SelectDesc), ctypes.POINTER(u64)]
+        L.cg_cache8_select.argtypes = [kvp, c8p, ctypes.POINTER(Cache8SelectDesc), vp, vp, vp, vp, vp, vp, u64, vp]
+        L.cg_cache8_evict.argtypes = [kvp, c8p, ctypes.POINTER(Cache8EvictDesc), vp, vp, vp, vp, vp, kvp, vp, vp, vp, vp,
+                                      vp, vp, vp]
         L.cg_spectral_workspace_size.argtypes = [ctypes.POINTER(KvDesc), ctypes.POINTER(StatsDesc), i32,
                                                  ctypes.POINTER(u64)]
         L.cg_spectral_stats.argtypes = [ctypes.POINTER(KvDesc), ctypes.POINTER(StatsDesc), vp, vp, vp, vp, vp, vp,
@@ -110,6 +149,8 @@ def lib():
         L.cg_last_cuda_error.restype = ctypes.c_char_p
         for name in ("cg_sizes_for", "cg_gauge_build", "cg_gauge_grad", "cg_adamw_step", "cg_group_gram",
                      "cg_encode", "cg_decode", "cg_decode_attention_workspace_size", "cg_decode_attention",
+                     "cg_cache8_sizes_for", "cg_cache8_append", "cg_cache8_attention_workspace_size",
+                     "cg_cache8_attention", "cg_cache8_select_workspace_size", "cg_cache8_select", "cg_cache8_evict",
                      "cg_spectral_workspace_size",
                      "cg_spectral_stats", "cg_spectral_stats_noalloc", "cg_selftest_wait_timeout",
                      "cg_sync_status"):
@@ -295,6 +336,139 @@ def cg_decode_attention(kvd, codec, at, q, codes, scales, zeros, G, out, workspa
                                      workspace.numel() * workspace.element_size(), _stream(stream)),
            "cg_decode_attention")
     return out
+
+
+def cache8_desc(code=CACHE8_INT8, tb=16):
+    return Cache8Desc(code, tb)
+
+
+def cache8_attn_desc(q_heads, max_tokens, q_tokens=1, layer0=0, n_layers=1, scale=None, d_head=128, n_select=0,
+                     accumulate=False):
+    return Cache8AttnDesc(q_heads, q_tokens, layer0, n_layers, max_tokens, n_select, int(accumulate),
+                          (1.0 / d_head ** 0.5) if scale is None else scale)
+
+
+def cache8_select_desc(q_heads, max_tokens, n_select, q_tokens=1, sink_blocks=1, recent_blocks=1, layer0=0, n_layers=1):
+    return Cache8SelectDesc(q_heads, q_tokens, layer0, n_layers, max_tokens, n_select, sink_blocks, recent_blocks)
+
+
+def cache8_evict_desc(keep_blocks, sink_blocks=1, recent_blocks=1, layer0=0, n_layers=1):
+    return Cache8EvictDesc(layer0, n_layers, keep_blocks, sink_blocks, recent_blocks)
+
+
+def cg_cache8_sizes_for(kvd, c8):
+    """(bytes of codes, scales, bytes of bounds, entries of mass) of an 8-bit block-scaled cache."""
+    out = Cache8Sizes()
+    _check(lib().cg_cache8_sizes_for(ctypes.byref(kvd), ctypes.byref(c8), ctypes.byref(out)), "cg_cache8_sizes_for")
+    return int(out.code_bytes), int(out.scale_count), int(out.bound_bytes), int(out.mass_count)
+
+
+def alloc_cache8(kvd, c8, device="cuda"):
+    """Caller-owned buffers of an empty cache: codes uint8 [L, 2, B, H, T, d], scales fp32
+    [L, 2, B, H, T/tb], bounds int8 [L, B, H, T/tb, 2, d], mass fp32 [L, B, H, T/tb]."""
+    cg_cache8_sizes_for(kvd, c8)
+    L, B, H, T, d, nb = kvd.layers, kvd.batch, kvd.heads, kvd.tokens, kvd.d_head, kvd.tokens // c8.tb
+    return (torch.zeros((L, 2, B, H, T, d), dtype=torch.uint8, device=device),
+            torch.zeros((L, 2, B, H, nb), dtype=torch.float32, device=device),
+            torch.zeros((L, B, H, nb, 2, d), dtype=torch.int8, device=device),
+            torch.zeros((L, B, H, nb), dtype=torch.float32, device=device))
+
+
+def _here(stream, *tensors):
+    """Stream pointer of a call whose tensors lie on the current device."""
+    dev = torch.cuda.current_device()
+    s = torch.cuda.current_stream(dev) if stream is None else stream
+    if s.device.index != dev:
+        raise ValueError("the stream is on cuda:%d, the current device is cuda:%d" % (s.device.index, dev))
+    for t in tensors:
+        if t is not None and t.is_cuda and t.get_device() != dev:
+            raise ValueError("a tensor is on cuda:%d, the current device is cuda:%d" % (t.get_device(), dev))
+    return ctypes.c_void_p(s.cuda_stream)
+
+
+def cg_cache8_append(kvd, c8, layer0, new, pos, counts, codes, scales, bounds, stream=None):
+    """Append new bf16 [n_layers, 2, B, H, n, d] at positions pos int32 [B]; of the n tokens sequence
+    b takes counts[b] (int32 [B], None: all); bounds may be None."""
+    cb, sc, bb, _ = cg_cache8_sizes_for(kvd, c8)
+    if new.dim() != 6 or tuple(new.shape[1:4]) != (2, kvd.batch, kvd.heads) or new.shape[5] != kvd.d_head:
+        raise ValueError("new must be [n_layers, 2, %d, %d, n, %d], got %s"
+                         % (kvd.batch, kvd.heads, kvd.d_head, tuple(new.shape)))
+    if new.numel() == 0:
+        return
+    _check(lib().cg_cache8_append(ctypes.byref(kvd), ctypes.byref(c8), int(layer0), new.shape[0], new.shape[4],
+                                  _ptr(new, torch.bfloat16, "new"), _ptr(pos, torch.int32, "pos", kvd.batch),
+                                  _ptr(counts, torch.int32, "counts", kvd.batch), _ptr(codes, torch.uint8, "codes", cb),
+                                  _ptr(scales, torch.float32, "scales", sc), _ptr(bounds, torch.int8, "bounds", bb),
+                                  _here(stream, new, pos, counts, codes, scales, bounds)), "cg_cache8_append")
+
+
+def cg_cache8_attention_workspace_size(kvd, c8, at, want_mass=False):
+    out = ctypes.c_uint64()
+    _check(lib().cg_cache8_attention_workspace_size(ctypes.byref(kvd), ctypes.byref(c8), ctypes.byref(at),
+                                                    int(bool(want_mass)), ctypes.byref(out)),
+           "cg_cache8_attention_workspace_size")
+    return int(out.value)
+
+
+def cg_cache8_attention(kvd, c8, at, q, codes, scales, lens, out, workspace, sel=None, mass=None, stream=None):
+    """Attention of the newest q_tokens tokens over the 8-bit cache: q bf16 [n_layers, B, Hq, q_tokens, d] ->
+    out fp32 of the same shape; sel int32 [n_layers, B, H, q_tokens, n_select] restricts it to listed
+    blocks; mass fp32 [L, B, H, T/tb] receives every block's softmax weight."""
+    cb, sc, _, mc = cg_cache8_sizes_for(kvd, c8)
+    rows = at.n_layers * kvd.batch * at.q_tokens
+    nq = rows * at.q_heads * kvd.d_head
+    _check(lib().cg_cache8_attention(ctypes.byref(kvd), ctypes.byref(c8), ctypes.byref(at),
+                                     _ptr(q, torch.bfloat16, "q", nq), _ptr(codes, torch.uint8, "codes", cb),
+                                     _ptr(scales, torch.float32, "scales", sc),
+                                     _ptr(lens, torch.int32, "lens", kvd.batch),
+                                     _ptr(sel, torch.int32, "sel", rows * kvd.heads * at.n_select),
+                                     _ptr(out, torch.float32, "out", nq), _ptr(mass, torch.float32, "mass", mc),
+                                     _ptr(workspace, torch.uint8, "workspace"), workspace.numel(),
+                                     _here(stream, q, codes, scales, lens, sel, out, mass, workspace)),
+           "cg_cache8_attention")
+    return out
+
+
+def cg_cache8_select_workspace_size(kvd, c8, sd):
+    out = ctypes.c_uint64()
+    _check(lib().cg_cache8_select_workspace_size(ctypes.byref(kvd), ctypes.byref(c8), ctypes.byref(sd),
+                                                 ctypes.byref(out)), "cg_cache8_select_workspace_size")
+    return int(out.value)
+
+
+def cg_cache8_select(kvd, c8, sd, q, scales, bounds, lens, sel, workspace, stream=None):
+    """The n_select blocks of each KV head and query token whose bounds promise the largest scores:
+    q bf16 [n_layers, B, Hq, q_tokens, d] -> sel int32 [n_layers, B, H, q_tokens, n_select]."""
+    _, sc, bb, _ = cg_cache8_sizes_for(kvd, c8)
+    rows = sd.n_layers * kvd.batch * sd.q_tokens
+    _check(lib().cg_cache8_select(ctypes.byref(kvd), ctypes.byref(c8), ctypes.byref(sd),
+                                  _ptr(q, torch.bfloat16, "q", rows * sd.q_heads * kvd.d_head),
+                                  _ptr(scales, torch.float32, "scales", sc), _ptr(bounds, torch.int8, "bounds", bb),
+                                  _ptr(lens, torch.int32, "lens", kvd.batch),
+                                  _ptr(sel, torch.int32, "sel", rows * kvd.heads * sd.n_select),
+                                  _ptr(workspace, torch.uint8, "workspace"), workspace.numel(),
+                                  _here(stream, q, scales, bounds, lens, sel, workspace)), "cg_cache8_select")
+    return sel
+
+
+def cg_cache8_evict(kvd, c8, ev, lens, codes, scales, bounds, mass, to_kvd, to_codes, to_scales, to_bounds, to_mass,
+                    to_lens, kept, stream=None):
+    """Move the blocks with the largest attention weight to another cache (bounds and to_bounds may
+    both be None); kept int32 [n_layers, B, H, keep_blocks] receives their indices."""
+    cb, sc, bb, mc = cg_cache8_sizes_for(kvd, c8)
+    tcb, tsc, tbb, tmc = cg_cache8_sizes_for(to_kvd, c8)
+    _check(lib().cg_cache8_evict(ctypes.byref(kvd), ctypes.byref(c8), ctypes.byref(ev),
+                                 _ptr(lens, torch.int32, "lens", kvd.batch), _ptr(codes, torch.uint8, "codes", cb),
+                                 _ptr(scales, torch.float32, "scales", sc), _ptr(bounds, torch.int8, "bounds", bb),
+                                 _ptr(mass, torch.float32, "mass", mc), ctypes.byref(to_kvd),
+                                 _ptr(to_codes, torch.uint8, "to_codes", tcb),
+                                 _ptr(to_scales, torch.float32, "to_scales", tsc),
+                                 _ptr(to_bounds, torch.int8, "to_bounds", tbb),
+                                 _ptr(to_mass, torch.float32, "to_mass", tmc),
+                                 _ptr(to_lens, torch.int32, "to_lens", kvd.batch),
+                                 _ptr(kept, torch.int32, "kept", ev.n_layers * kvd.batch * kvd.heads * ev.keep_blocks),
+                                 _here(stream, lens, codes, scales, bounds, mass, to_codes, to_scales, to_bounds,
+                                       to_mass, to_lens, kept)), "cg_cache8_evict")
 
 
 def cg_spectral_workspace_size(kvd, st, want_grad):
