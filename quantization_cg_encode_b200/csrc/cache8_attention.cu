@@ -12,17 +12,18 @@
 //           per row that puts its largest element into [2^14, 2^15): bf16 values are exact in
 //           fp16 down to 2^-29 of the row's largest;
 //   values  A = 16 channels x 16 tokens of value codes; B = p as two fp16 terms (2^-22).
-// The order of channels within a contraction is free, so a thread's codes come as 16-byte
-// pieces of the cache's rows, with no exchange between threads; B of the second product is the
-// scores' layout transposed (movmatrix).
+// The order of channels within a contraction is free, so ldmatrix moves the bytes as 16-bit
+// pairs and no thread exchanges codes with another; B of the second product is the scores'
+// layout transposed (movmatrix).
 //
 // The value scale is a power of two, 2^v: p s_V = 2^(x + v) is kept relative to its own running
 // maximum M', so that no ratio of scales costs fp16 range, and the sum of p relative to M:
 //   out = (sum 2^(x + v - M') code) / (sum 2^(x - M)) 2^(M' - M).
 // M and M' follow the maxima lazily (they move when a value is 2^8 above).
 //
-// A warp owns 16-token tiles; the warps of a CTA share a run of tiles (a split) and merge in
-// shared memory; a second kernel merges the splits.
+// A warp owns 16-token tiles, which it fetches by itself (cp.async, a ring of kStages tiles, so
+// that the warps never wait for one another); the warps of a CTA share a run of tiles (a split)
+// and merge in shared memory; a second kernel merges the splits.
 #include "cache8.cuh"
 
 namespace cg {
@@ -30,6 +31,7 @@ namespace cg {
 namespace {
 
 constexpr int kWarps = 8;
+constexpr int kStages = 3;
 constexpr int kMaxSplits = 256;
 constexpr int kSms = 148;               // what the split is sized for
 constexpr float kNone = -1.0e30f;       // a running maximum that has seen nothing
@@ -46,7 +48,30 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-__device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+// 16 bytes (or 4) from global to shared memory, asynchronously; `bytes` 0 writes zeros
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+// Where 16-byte piece `ch` of row `row` of a tile stands: rows of 128 (64) bytes, the pieces permuted
+// so that the same piece of eight rows falls into different banks.
+template <int D>
+__device__ __forceinline__ uint32_t piece_at(int row, int ch) {
+  return (uint32_t)(row * D + ((ch ^ (D == 128 ? row & 7 : (row >> 1) & 3)) << 4));
+}
 // maximum over the eight lanes that share lane % 4
 __device__ __forceinline__ float column_max(float v) {
 #pragma unroll
@@ -68,9 +93,12 @@ __device__ __forceinline__ int live_tiles(const Cache8AttnArgs& a, int n) {
 
 template <int D, int CODE, int NT, bool SPARSE, bool MASS>
 __global__ void __launch_bounds__(kWarps * 32) cache8_attn_kernel(Cache8AttnArgs a) {
-  constexpr int R = 8 * NT, HALVES = D / 64, VW = D / 32;  // VW: words of a thread's value codes of one token
+  constexpr int R = 8 * NT, CH = D / 16, TILE = 16 * D;  // CH: 16-byte pieces of a row
   __shared__ float s_m[kWarps][R], s_mv[kWarps][R], s_l[kWarps][R];
-  extern __shared__ float s_o[];  // [kWarps][R][D]
+  __shared__ float s_scale[kWarps][kStages][2];
+  // the warps' tiles [kWarps][kStages][key, value][TILE], then their outputs fp32 [kWarps][R][D]
+  extern __shared__ __align__(128) unsigned char dyn[];
+  float* s_o = reinterpret_cast<float*>(dyn);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const int split = blockIdx.x % a.splits;
   long long u = blockIdx.x / a.splits;
@@ -104,42 +132,36 @@ __global__ void __launch_bounds__(kWarps * 32) cache8_attn_kernel(Cache8AttnArgs
   const int tb_shift = 31 - __clz(a.c.tb);
 
   // q as the scores' B operand, its row's power of two, and what each column's rows see
-  uint32_t bq[NT][4 * HALVES][2];
+  uint32_t bq[NT][CH][2];
   float qs[NT][2];
   int lim[NT][2];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     const int r = rt * R + nt * 8 + g;
     const uint16_t* qrow = a.q + (first + (long long)min(r, rows - 1) * step) * D;
-    uint4 raw[HALVES][2];
+    uint2 raw[CH];  // four channels of every piece
     float m = 0.0f;
 #pragma unroll
-    for (int hh = 0; hh < HALVES; ++hh)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        raw[hh][j] = r < rows ? *reinterpret_cast<const uint4*>(qrow + 64 * hh + 16 * c + 8 * j) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) m = fmaxf(m, fmaxf(fabsf(bf16lo(word(raw[hh][j], i))), fabsf(bf16hi(word(raw[hh][j], i)))));
-      }
+    for (int j = 0; j < CH; ++j) {
+      raw[j] = r < rows ? *reinterpret_cast<const uint2*>(qrow + 16 * j + 4 * c) : make_uint2(0, 0);
+      m = fmaxf(m, fmaxf(fmaxf(fabsf(bf16lo(raw[j].x)), fabsf(bf16hi(raw[j].x))), fmaxf(fabsf(bf16lo(raw[j].y)), fabsf(bf16hi(raw[j].y)))));
+    }
     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
     const int e = max((int)(__float_as_uint(m) >> 23) - 127, -100) - 14;  // m 2^-e in [2^14, 2^15)
     const float up = two_to(-e);
 #pragma unroll
-    for (int hh = 0; hh < HALVES; ++hh)
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const uint32_t p0 = word(raw[hh][w >> 1], 2 * (w & 1)), p1 = word(raw[hh][w >> 1], 2 * (w & 1) + 1);
-        const float v0 = bf16lo(p0) * up, v1 = bf16hi(p0) * up, v2 = bf16lo(p1) * up, v3 = bf16hi(p1) * up;
-        __half2 f0, f1;
-        if (CODE == kCache8Int8) {
-          f0 = __floats2half2_rn(v0, v2), f1 = __floats2half2_rn(v1, v3);
-        } else {
-          f0 = __floats2half2_rn(v0, v1), f1 = __floats2half2_rn(v2, v3);
-        }
-        bq[nt][4 * hh + w][0] = *reinterpret_cast<uint32_t*>(&f0);
-        bq[nt][4 * hh + w][1] = *reinterpret_cast<uint32_t*>(&f1);
+    for (int j = 0; j < CH; ++j) {
+      const float v0 = bf16lo(raw[j].x) * up, v1 = bf16hi(raw[j].x) * up, v2 = bf16lo(raw[j].y) * up, v3 = bf16hi(raw[j].y) * up;
+      __half2 f0, f1;  // the order in which codes_to_f16 gives the four codes
+      if (CODE == kCache8Int8) {
+        f0 = __floats2half2_rn(v0, v2), f1 = __floats2half2_rn(v1, v3);
+      } else {
+        f0 = __floats2half2_rn(v0, v1), f1 = __floats2half2_rn(v2, v3);
       }
+      bq[nt][j][0] = *reinterpret_cast<uint32_t*>(&f0);
+      bq[nt][j][1] = *reinterpret_cast<uint32_t*>(&f1);
+    }
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int col = 2 * c + j, rc = rt * R + nt * 8 + col;
@@ -164,53 +186,72 @@ __global__ void __launch_bounds__(kWarps * 32) cache8_attn_kernel(Cache8AttnArgs
   }
 
   const int* list = SPARSE ? a.sel + (u * a.nq + qi) * a.n_select : nullptr;
-  for (int tile = tile0 + warp; tile < tile1; tile += kWarps) {
-    int t0 = tile * 16;
-    if (SPARSE) {
-      const int blk = list[t0 >> tb_shift];
-      if (blk < 0 || blk > (end - 1) >> tb_shift || end == 0) continue;  // warp-uniform
-      t0 = (blk << tb_shift) + (t0 & (a.c.tb - 1));
-      if (t0 >= end) continue;
-    }
-    const bool full = t0 + 16 <= end;  // else the codes behind the end may be anything: not read
-    uint4 kr[2][HALVES];
-    uint32_t vr[4][VW];
+  const uint32_t ring = smem_u32(dyn) + warp * (kStages * 2 * TILE);
+  const int n_mine = (tile1 - tile0 - warp + kWarps - 1) / kWarps;  // this warp's tiles: tile0 + warp + i kWarps
+  // the block that tile i lies in, or the same for every tile of the warp: its first token, -1 if it has none to see
+  auto listed = [&](int i) { return i < n_mine ? list[((tile0 + warp + i * kWarps) * 16) >> tb_shift] : -1; };
+  auto first_token = [&](int i, int blk) {
+    const int t = (tile0 + warp + i * kWarps) * 16;
+    if (!SPARSE) return t;
+    if (blk < 0 || end == 0 || blk > (end - 1) >> tb_shift) return -1;
+    const int t0 = (blk << tb_shift) + (t & (a.c.tb - 1));
+    return t0 < end ? t0 : -1;
+  };
+  // codes behind the end may be anything: zeros stand for them
+  auto fetch = [&](int i, int t0) {
+    if (i < n_mine && t0 >= 0) {
+      const uint32_t dst = ring + (i % kStages) * (2 * TILE);
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int hh = 0; hh < HALVES; ++hh) {
-        const int t = t0 + g + 8 * j;
-        kr[j][hh] = full || t < end ? *reinterpret_cast<const uint4*>(kc + (long long)t * D + 64 * hh + 16 * c) : make_uint4(0, 0, 0, 0);
+      for (int j = 0; j < CH / 2; ++j) {
+        const int row = lane / CH + j * (32 / CH), ch = lane % CH;
+        const int bytes = t0 + row < end ? 16 : 0;
+        const long long at = (long long)(bytes ? t0 + row : t0) * D + 16 * ch;
+        copy16(dst + piece_at<D>(row, ch), kc + at, bytes);
+        copy16(dst + TILE + piece_at<D>(row, ch), vc + at, bytes);
       }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int t = t0 + 2 * c + (j & 1) + 8 * (j >> 1);
-      const uint8_t* p = vc + (long long)t * D + (D / 8) * g;
-      if constexpr (VW == 4) {
-        const uint4 v = full || t < end ? *reinterpret_cast<const uint4*>(p) : make_uint4(0, 0, 0, 0);
-        vr[j][0] = v.x, vr[j][1] = v.y, vr[j][2] = v.z, vr[j][3] = v.w;
-      } else {
-        const uint2 v = full || t < end ? *reinterpret_cast<const uint2*>(p) : make_uint2(0, 0);
-        vr[j][0] = v.x, vr[j][1] = v.y;
-      }
+      if (lane < 2) copy4(smem_u32(&s_scale[warp][i % kStages][lane]), (lane ? vs : ks) + (t0 >> tb_shift));
     }
-    const float kscale = ks[t0 >> tb_shift];
-    const float vexp = (float)((int)(__float_as_uint(vs[t0 >> tb_shift]) >> 23) - 127);
+    copies_commit();
+  };
+  int starts[kStages];  // first tokens of the tiles in flight, the next one first
+#pragma unroll
+  for (int i = 0; i < kStages; ++i) starts[i] = first_token(i, SPARSE ? listed(i) : 0);
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) fetch(i, starts[i]);
+  const int lrow = lane & 15, lch = lane >> 4;  // ldmatrix: rows 0-7, 8-15 of a piece, then of the next
+  int blk_ahead = SPARSE ? listed(kStages) : 0;
+
+  for (int i = 0; i < n_mine; ++i) {
+    const int tile = tile0 + warp + i * kWarps, t0 = starts[0], st = i % kStages;
+    fetch(i + kStages - 1, starts[kStages - 1]);
+    copies_wait<kStages - 1>();
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j + 1 < kStages; ++j) starts[j] = starts[j + 1];
+    starts[kStages - 1] = first_token(i + kStages, blk_ahead);
+    if (SPARSE) blk_ahead = listed(i + kStages + 1);
+    if (SPARSE && t0 < 0) continue;  // warp-uniform
+    const uint32_t kt = ring + st * (2 * TILE), vt = kt + TILE;
+    const float kscale = s_scale[warp][st][0];
+    const float vexp = (float)((int)(__float_as_uint(s_scale[warp][st][1]) >> 23) - 127);
 
     // scores of 16 tokens x R rows
     float s[NT][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.0f;
 #pragma unroll
-    for (int hh = 0; hh < HALVES; ++hh)
+    for (int jj = 0; jj < CH / 2; ++jj) {
+      uint32_t w[4];  // token g, g + 8 of piece 2 jj, then of the next
+      ldmatrix_x4(w, kt + piece_at<D>(lrow, 2 * jj + lch));
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
+      for (int k = 0; k < 2; ++k) {
         uint32_t af[4];
-        codes_to_f16<CODE>(word(kr[0][hh], w), af[0], af[2]);
-        codes_to_f16<CODE>(word(kr[1][hh], w), af[1], af[3]);
+        codes_to_f16<CODE>(w[2 * k], af[0], af[2]);
+        codes_to_f16<CODE>(w[2 * k + 1], af[1], af[3]);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma_f16_16816(s[nt], af, bq[nt][4 * hh + w][0], bq[nt][4 * hh + w][1]);
+        for (int nt = 0; nt < NT; ++nt) mma_f16_16816(s[nt], af, bq[nt][2 * jj + k][0], bq[nt][2 * jj + k][1]);
       }
+    }
     // s[nt][0..3]: token g (0, 1) or g + 8 (2, 3), row 2c + (index & 1)
     bool over = false;
 #pragma unroll
@@ -269,21 +310,27 @@ __global__ void __launch_bounds__(kWarps * 32) cache8_attn_kernel(Cache8AttnArgs
     }
     // o[channel][row] += codes^T p
 #pragma unroll
-    for (int w = 0; w < VW; ++w)
+    for (int jj = 0; jj < CH / 2; ++jj) {
+      uint32_t w[4];  // tokens 2c, 2c + 1, then 2c + 8, 2c + 9, of channels 2g, 2g + 1 of piece 2 jj; of the next
+      ldmatrix_x4_trans(w, vt + piece_at<D>(lrow, 2 * jj + lch));
 #pragma unroll
-      for (int p = 0; p < 2; ++p) {
+      for (int k = 0; k < 2; ++k) {
         uint32_t af[4];
-        const uint32_t pick = CODE == kCache8Int8 ? (p ? 0x7632u : 0x5410u) : (p ? 0x7362u : 0x5140u);
-        codes_to_f16<CODE>(__byte_perm(vr[0][w], vr[1][w], pick), af[0], af[1]);
-        codes_to_f16<CODE>(__byte_perm(vr[2][w], vr[3][w], pick), af[2], af[3]);
+        if (CODE == kCache8E4m3) w[2 * k] = __byte_perm(w[2 * k], 0, 0x3120), w[2 * k + 1] = __byte_perm(w[2 * k + 1], 0, 0x3120);
+        codes_to_f16<CODE>(w[2 * k], af[0], af[1]);
+        codes_to_f16<CODE>(w[2 * k + 1], af[2], af[3]);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          mma_f16_16816(o[nt][2 * w + p], af, bhi[nt][0], bhi[nt][1]);
-          mma_f16_16816(o[nt][2 * w + p], af, blo[nt][0], blo[nt][1]);
+          mma_f16_16816(o[nt][2 * jj + k], af, bhi[nt][0], bhi[nt][1]);
+          mma_f16_16816(o[nt][2 * jj + k], af, blo[nt][0], blo[nt][1]);
         }
       }
+    }
+    __syncwarp();  // the stage is free for the next fetch
   }
 
+  copies_wait<0>();
+  __syncthreads();  // the tiles' memory now takes the outputs
   // merge the warps: o relative to the CTA's maxima
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
@@ -294,7 +341,7 @@ __global__ void __launch_bounds__(kWarps * 32) cache8_attn_kernel(Cache8AttnArgs
       if (g == 0) s_m[warp][r] = m_run[nt][j], s_mv[warp][r] = mv_run[nt][j], s_l[warp][r] = l;
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) {
-        const int ch = (D / 8) * g + 2 * i;  // tile i = 2 w + p: channels 4 w + 2 p and the next
+        const int ch = 16 * i + 2 * g;
         s_o[(warp * R + r) * D + ch] = o[nt][i][j];
         s_o[(warp * R + r) * D + ch + 1] = o[nt][i][j + 2];
       }
@@ -423,7 +470,8 @@ void layout(Cache8AttnArgs& a, char* base, bool want_mass, uint64_t& bytes) {
 
 template <int D, int CODE, int NT, bool SPARSE, bool MASS>
 cudaError_t launch_one(const Cache8AttnArgs& a, cudaStream_t st) {
-  const size_t smem = sizeof(float) * kWarps * 8 * NT * D;
+  const size_t tiles = (size_t)kWarps * kStages * 32 * D, outputs = sizeof(float) * kWarps * 8 * NT * D;
+  const size_t smem = tiles > outputs ? tiles : outputs;
   auto kern = cache8_attn_kernel<D, CODE, NT, SPARSE, MASS>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
