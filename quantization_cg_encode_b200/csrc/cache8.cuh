@@ -50,13 +50,14 @@ struct Cache8AttnArgs {
   float* mass;             // or null
   // set by the launcher
   int nt;                  // query rows of a CTA / 8
-  int row_tiles, splits, tiles_per_split;
-  float* part;             // [row][split][d + 4] {max, max with value scale, sum, -, o[d]}
+  int row_tiles, ctas;
+  float* part;             // [cta][2][8 nt][d + 4] {max, max with value scale, sum, -, o[d]}
+  void* tails;             // [cta]
   float2* tile_mass;       // [row][16-token tile] {sum, its reference}
   float2* stats;           // [row] {max, 1 / sum}
 };
 uint64_t cache8_attn_workspace(Cache8AttnArgs a, bool want_mass);
-bool cache8_attn_fits(Cache8AttnArgs a);
+bool cache8_attn_fits(const Cache8AttnArgs& a, bool want_mass);
 cudaError_t launch_cache8_attention(Cache8AttnArgs a, void* workspace, cudaStream_t st);
 
 struct Cache8SelectArgs {
@@ -92,6 +93,25 @@ struct Cache8EvictArgs {
 };
 bool cache8_evict_fits(const Cache8EvictArgs& a);
 cudaError_t launch_cache8_evict(const Cache8EvictArgs& a, cudaStream_t st);
+
+// Launch that may begin while the kernel before it on the stream still runs; such a kernel calls
+// previous_kernel_done() in every thread before it touches memory.
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, P(args)...);
+}
+__device__ __forceinline__ void previous_kernel_done() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void dependents_may_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // The least e >= -126 with amax <= top 2^e, top = 127 (int8) or 448 (e4m3), for finite amax >= 0.
 // With amax = m 2^x, m in [1, 2): 127 = (127/64) 2^6 and 448 = (7/4) 2^8.

@@ -58,7 +58,7 @@ cg_status check_attn8(const cg_kv_desc* kv, const cg_cache8_desc* c8, const cg_c
   a.n_select = at->n_select;
   a.accumulate = at->accumulate;
   a.scale = at->scale;
-  return cache8_attn_fits(a) ? CG_OK : CG_ERR_TOO_LARGE;
+  return cache8_attn_fits(a, want_mass) ? CG_OK : CG_ERR_TOO_LARGE;
 }
 
 cg_status check_select8(const cg_kv_desc* kv, const cg_cache8_desc* c8, const cg_cache8_select_desc* sd, Cache8SelectArgs& a) {

@@ -21,9 +21,12 @@
 //   out = (sum 2^(x + v - M') code) / (sum 2^(x - M)) 2^(M' - M).
 // M and M' follow the maxima lazily (they move when a value is 2^8 above).
 //
-// A warp owns 16-token tiles, which it fetches by itself (cp.async, a ring of kStages tiles, so
-// that the warps never wait for one another); the warps of a CTA share a run of tiles (a split)
-// and merge in shared memory; a second kernel merges the splits.
+// All tiles of the call (every unit's, a unit being the query rows of one layer, sequence and KV
+// head, 8 or 16 of them) stand in one row, of which every CTA takes an equal run, so that ragged
+// lengths and odd head counts leave no CTA waiting.  Within a run a warp fetches its tiles by
+// itself (cp.async, a ring of kStages tiles); at a unit's end the warps merge in shared memory.
+// A unit that lies in one run goes out as it is; the pieces of the others go to the workspace
+// and a second kernel merges them.
 #include "cache8.cuh"
 
 namespace cg {
@@ -32,8 +35,8 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kStages = 3;
-constexpr int kMaxSplits = 256;
-constexpr int kSms = 148;               // what the split is sized for
+constexpr int kSms = 148;               // what the number of CTAs is sized for
+constexpr int kLeastRun = kWarps;       // tiles: one a warp
 constexpr float kNone = -1.0e30f;       // a running maximum that has seen nothing
 constexpr float kLag = 8.0f;            // how far a value may lie above the running maximum
 constexpr float kShift = 7.0f;          // 2^kShift p' <= 2^15 fits fp16
@@ -84,349 +87,446 @@ __device__ __forceinline__ float column_sum(float v) {
   return v;
 }
 __device__ __forceinline__ int clamped_len(const Cache8AttnArgs& a, int b) { return max(0, min(a.lens[b], a.max_tokens)); }
-// 16-token tiles that the rows of a unit have to look at
-__device__ __forceinline__ int live_tiles(const Cache8AttnArgs& a, int n) {
+// 16-token tiles of a unit: all that it may see, or all that are listed
+__device__ __forceinline__ int unit_tiles(const Cache8AttnArgs& a, int b) {
+  const int n = clamped_len(a, b);
   return a.n_select ? (n ? a.n_select * (a.c.tb >> 4) : 0) : (n + 15) >> 4;
 }
+
+// A unit whose last piece is in this CTA's run and whose first is not
+struct Tail {
+  long long row0;  // its first output row
+  int step;        // distance of its rows
+  int rows;
+  int pieces;      // this one included; 0: the CTA has no such unit
+  int pad;
+};
 
 }  // namespace
 
 template <int D, int CODE, int NT, bool SPARSE, bool MASS>
-__global__ void __launch_bounds__(kWarps * 32) cache8_attn_kernel(Cache8AttnArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, D == 128 && NT == 2 ? 1 : 2) cache8_attn_kernel(Cache8AttnArgs a) {
   constexpr int R = 8 * NT, CH = D / 16, TILE = 16 * D;  // CH: 16-byte pieces of a row
   __shared__ float s_m[kWarps][R], s_mv[kWarps][R], s_l[kWarps][R];
+  __shared__ float s_w[kWarps][R], s_fin[R][3];
   __shared__ float s_scale[kWarps][kStages][2];
+  __shared__ long long s_sum[kWarps], s_before;
+  __shared__ int s_batch;
   // the warps' tiles [kWarps][kStages][key, value][TILE], then their outputs fp32 [kWarps][R][D]
   extern __shared__ __align__(128) unsigned char dyn[];
   float* s_o = reinterpret_cast<float*>(dyn);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-  const int split = blockIdx.x % a.splits;
-  long long u = blockIdx.x / a.splits;
-  const int rt = (int)(u % a.row_tiles);
-  u /= a.row_tiles;
-  const int qi = SPARSE ? (int)(u % a.nq) : 0;  // the query token of a sparse unit
-  if (SPARSE) u /= a.nq;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
   const int H = a.c.k.H, B = a.c.k.B;
-  const int h = (int)(u % H), b = (int)((u / H) % B), lz = (int)(u / H / B);
   const int rows = SPARSE ? a.gq : a.gq * a.nq;
-  const int n = clamped_len(a, b);
-  const int tiles = live_tiles(a, n);
-  const int tile0 = split * a.tiles_per_split, tile1 = min(tiles, tile0 + a.tiles_per_split);
-  // row r of the unit is row `first + r step` of the [nl][B][hq][nq] rows
-  const long long first = (u * a.gq) * a.nq + qi, step = SPARSE ? a.nq : 1;
-  if (tile0 >= tile1) {
-    if (a.splits == 1)  // nothing to see: zeros
-      for (int e = threadIdx.x; e < R * D; e += kWarps * 32) {
-        const int r = rt * R + e / D;
-        if (r < rows) a.out[(first + r * step) * D + e % D] = 0.0f;
-        if (MASS && r < rows && e % D == 0) a.stats[first + r * step] = make_float2(0.0f, 0.0f);
-      }
-    return;
-  }
-  const long long ks_slice = (((long long)(a.l0 + lz) * 2 + 0) * B + b) * H + h;
-  const long long vs_slice = (((long long)(a.l0 + lz) * 2 + 1) * B + b) * H + h;
-  const uint8_t* kc = a.codes + ks_slice * a.c.k.T * D;
-  const uint8_t* vc = a.codes + vs_slice * a.c.k.T * D;
-  const float* ks = a.scales + ks_slice * a.c.blocks();
-  const float* vs = a.scales + vs_slice * a.c.blocks();
+  const int per_batch = H * (SPARSE ? a.nq : 1) * a.row_tiles;  // units of one layer and sequence
   const int tb_shift = 31 - __clz(a.c.tb);
+  dependents_may_launch();
+  previous_kernel_done();
 
-  // q as the scores' B operand, its row's power of two, and what each column's rows see
-  uint32_t bq[NT][CH][2];
-  float qs[NT][2];
-  int lim[NT][2];
+  // Tiles of one layer: the sum over the batch, 256 sequences at a time; with it the run of this
+  // CTA and the sequence in which it begins.
+  auto block_scan = [&](long long v, long long& total) {  // exclusive prefix over the CTA
+    long long incl = v;
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const int r = rt * R + nt * 8 + g;
-    const uint16_t* qrow = a.q + (first + (long long)min(r, rows - 1) * step) * D;
-    uint2 raw[CH];  // four channels of every piece
-    float m = 0.0f;
-#pragma unroll
-    for (int j = 0; j < CH; ++j) {
-      raw[j] = r < rows ? *reinterpret_cast<const uint2*>(qrow + 16 * j + 4 * c) : make_uint2(0, 0);
-      m = fmaxf(m, fmaxf(fmaxf(fabsf(bf16lo(raw[j].x)), fabsf(bf16hi(raw[j].x))), fmaxf(fabsf(bf16lo(raw[j].y)), fabsf(bf16hi(raw[j].y)))));
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += x;
     }
-    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    const int e = max((int)(__float_as_uint(m) >> 23) - 127, -100) - 14;  // m 2^-e in [2^14, 2^15)
-    const float up = two_to(-e);
+    __syncthreads();
+    if (lane == 31) s_sum[warp] = incl;
+    __syncthreads();
+    long long before = 0;
+    total = 0;
 #pragma unroll
-    for (int j = 0; j < CH; ++j) {
-      const float v0 = bf16lo(raw[j].x) * up, v1 = bf16hi(raw[j].x) * up, v2 = bf16lo(raw[j].y) * up, v3 = bf16hi(raw[j].y) * up;
-      __half2 f0, f1;  // the order in which codes_to_f16 gives the four codes
-      if (CODE == kCache8Int8) {
-        f0 = __floats2half2_rn(v0, v2), f1 = __floats2half2_rn(v1, v3);
-      } else {
-        f0 = __floats2half2_rn(v0, v1), f1 = __floats2half2_rn(v2, v3);
-      }
-      bq[nt][j][0] = *reinterpret_cast<uint32_t*>(&f0);
-      bq[nt][j][1] = *reinterpret_cast<uint32_t*>(&f1);
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) before += s_sum[w];
+      total += s_sum[w];
     }
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int col = 2 * c + j, rc = rt * R + nt * 8 + col;
-      qs[nt][j] = two_to(max(__shfl_sync(0xffffffffu, e, 4 * col), -126)) * (a.scale * 1.4426950408889634f);
-      const int i = SPARSE ? qi : rc % a.nq;
-      lim[nt][j] = rc < rows ? max(0, n - a.nq + 1 + i) : 0x7fffffff;  // columns beyond the rows are not stored
-    }
-  }
-  const int all_see = max(0, n - a.nq + 1 + (SPARSE ? qi : 0));  // tokens that every row sees
-  const int end = SPARSE ? all_see : n;                          // tokens that some row sees
-
-  float o[NT][D / 16][4];
-  float m_run[NT][2], mv_run[NT][2], l_run[NT][2];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-    for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) o[nt][i][j] = 0.0f;
-#pragma unroll
-    for (int j = 0; j < 2; ++j) m_run[nt][j] = mv_run[nt][j] = kNone, l_run[nt][j] = 0.0f;
-  }
-
-  const int* list = SPARSE ? a.sel + (u * a.nq + qi) * a.n_select : nullptr;
-  const uint32_t ring = smem_u32(dyn) + warp * (kStages * 2 * TILE);
-  const int n_mine = (tile1 - tile0 - warp + kWarps - 1) / kWarps;  // this warp's tiles: tile0 + warp + i kWarps
-  // the block that tile i lies in, or the same for every tile of the warp: its first token, -1 if it has none to see
-  auto listed = [&](int i) { return i < n_mine ? list[((tile0 + warp + i * kWarps) * 16) >> tb_shift] : -1; };
-  auto first_token = [&](int i, int blk) {
-    const int t = (tile0 + warp + i * kWarps) * 16;
-    if (!SPARSE) return t;
-    if (blk < 0 || end == 0 || blk > (end - 1) >> tb_shift) return -1;
-    const int t0 = (blk << tb_shift) + (t & (a.c.tb - 1));
-    return t0 < end ? t0 : -1;
+    return before + incl - v;
   };
-  // codes behind the end may be anything: zeros stand for them
-  auto fetch = [&](int i, int t0) {
-    if (i < n_mine && t0 >= 0) {
-      const uint32_t dst = ring + (i % kStages) * (2 * TILE);
-#pragma unroll
-      for (int j = 0; j < CH / 2; ++j) {
-        const int row = lane / CH + j * (32 / CH), ch = lane % CH;
-        const int bytes = t0 + row < end ? 16 : 0;
-        const long long at = (long long)(bytes ? t0 + row : t0) * D + 16 * ch;
-        copy16(dst + piece_at<D>(row, ch), kc + at, bytes);
-        copy16(dst + TILE + piece_at<D>(row, ch), vc + at, bytes);
-      }
-      if (lane < 2) copy4(smem_u32(&s_scale[warp][i % kStages][lane]), (lane ? vs : ks) + (t0 >> tb_shift));
+  long long layer_tiles = 0;
+  for (int b0 = 0; b0 < B; b0 += kWarps * 32) {
+    long long t;
+    block_scan(b0 + tid < B ? (long long)unit_tiles(a, b0 + tid) * per_batch : 0, t);
+    layer_tiles += t;
+  }
+  const long long total = layer_tiles * a.nl;
+  const long long run = max((long long)kLeastRun, (total + gridDim.x - 1) / gridDim.x);
+  const long long begin = min(total, blockIdx.x * run), end_all = min(total, begin + run);
+  int lz = 0, b = 0, idx = 0, tile0 = 0, tiles = 0;
+  long long unit_at = 0;  // the unit's first tile in the row of all tiles
+  if (begin < end_all) {
+    lz = (int)(begin / layer_tiles);
+    const long long rem = begin - lz * layer_tiles;
+    long long passed = 0;
+    for (int b0 = 0; b0 < B; b0 += kWarps * 32) {
+      const long long v = b0 + tid < B ? (long long)unit_tiles(a, b0 + tid) * per_batch : 0;
+      long long t;
+      const long long before = passed + block_scan(v, t);
+      if (before <= rem && rem < before + v) s_batch = b0 + tid, s_before = before;
+      passed += t;
     }
-    copies_commit();
-  };
-  int starts[kStages];  // first tokens of the tiles in flight, the next one first
-#pragma unroll
-  for (int i = 0; i < kStages; ++i) starts[i] = first_token(i, SPARSE ? listed(i) : 0);
-#pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) fetch(i, starts[i]);
-  const int lrow = lane & 15, lch = lane >> 4;  // ldmatrix: rows 0-7, 8-15 of a piece, then of the next
-  int blk_ahead = SPARSE ? listed(kStages) : 0;
+    __syncthreads();
+    b = s_batch;
+    tiles = unit_tiles(a, b);
+    idx = (int)((rem - s_before) / tiles);
+    unit_at = lz * layer_tiles + s_before + (long long)idx * tiles;
+    tile0 = (int)(begin - unit_at);
+  }
 
-  for (int i = 0; i < n_mine; ++i) {
-    const int tile = tile0 + warp + i * kWarps, t0 = starts[0], st = i % kStages;
-    fetch(i + kStages - 1, starts[kStages - 1]);
-    copies_wait<kStages - 1>();
-    __syncwarp();
-#pragma unroll
-    for (int j = 0; j + 1 < kStages; ++j) starts[j] = starts[j + 1];
-    starts[kStages - 1] = first_token(i + kStages, blk_ahead);
-    if (SPARSE) blk_ahead = listed(i + kStages + 1);
-    if (SPARSE && t0 < 0) continue;  // warp-uniform
-    const uint32_t kt = ring + st * (2 * TILE), vt = kt + TILE;
-    const float kscale = s_scale[warp][st][0];
-    const float vexp = (float)((int)(__float_as_uint(s_scale[warp][st][1]) >> 23) - 127);
+  Tail tail = {0, 0, 0, 0, 0};
+  for (long long at = begin; at < end_all;) {
+    const int rt = idx % a.row_tiles;
+    const int qi = SPARSE ? idx / a.row_tiles % a.nq : 0;  // the query token of a sparse unit
+    const int h = idx / a.row_tiles / (SPARSE ? a.nq : 1);
+    const long long u = ((long long)lz * B + b) * H + h;
+    const int n = clamped_len(a, b);
+    const int tile1 = (int)min((long long)tiles, tile0 + (end_all - at));
+    // row r of the unit is row `first + r step` of the [nl][B][hq][nq] rows
+    const long long first = u * a.gq * a.nq + qi, step = SPARSE ? a.nq : 1;
+    const long long ks_slice = (((long long)(a.l0 + lz) * 2 + 0) * B + b) * H + h;
+    const long long vs_slice = (((long long)(a.l0 + lz) * 2 + 1) * B + b) * H + h;
+    const uint8_t* kc = a.codes + ks_slice * a.c.k.T * D;
+    const uint8_t* vc = a.codes + vs_slice * a.c.k.T * D;
+    const float* ks = a.scales + ks_slice * a.c.blocks();
+    const float* vs = a.scales + vs_slice * a.c.blocks();
+    const int all_see = max(0, n - a.nq + 1 + (SPARSE ? qi : 0));  // tokens that every row sees
+    const int end = SPARSE ? all_see : n;                          // tokens that some row sees
 
-    // scores of 16 tokens x R rows
-    float s[NT][4];
+    const int* list = SPARSE ? a.sel + (u * a.nq + qi) * a.n_select : nullptr;
+    const uint32_t ring = smem_u32(dyn) + warp * (kStages * 2 * TILE);
+    const int n_mine = (tile1 - tile0 - warp + kWarps - 1) / kWarps;  // this warp's tiles: tile0 + warp + i kWarps
+    // the block that tile i lies in, and the tile's first token, -1 if it has none to see
+    auto listed = [&](int i) { return i < n_mine ? list[((tile0 + warp + i * kWarps) * 16) >> tb_shift] : -1; };
+    auto first_token = [&](int i, int blk) {
+      const int t = (tile0 + warp + i * kWarps) * 16;
+      if (!SPARSE) return t;
+      if (blk < 0 || end == 0 || blk > (end - 1) >> tb_shift) return -1;
+      const int t0 = (blk << tb_shift) + (t & (a.c.tb - 1));
+      return t0 < end ? t0 : -1;
+    };
+    // codes behind the end may be anything: zeros stand for them
+    auto fetch = [&](int i, int t0) {
+      if (i < n_mine && t0 >= 0) {
+        const uint32_t dst = ring + (i % kStages) * (2 * TILE);
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.0f;
+        for (int j = 0; j < CH / 2; ++j) {
+          const int row = lane / CH + j * (32 / CH), ch = lane % CH;
+          const int bytes = t0 + row < end ? 16 : 0;
+          const long long from = (long long)(bytes ? t0 + row : t0) * D + 16 * ch;
+          copy16(dst + piece_at<D>(row, ch), kc + from, bytes);
+          copy16(dst + TILE + piece_at<D>(row, ch), vc + from, bytes);
+        }
+        if (lane < 2) copy4(smem_u32(&s_scale[warp][i % kStages][lane]), (lane ? vs : ks) + (t0 >> tb_shift));
+      }
+      copies_commit();
+    };
+    int starts[kStages];  // first tokens of the tiles in flight, the next one first
 #pragma unroll
-    for (int jj = 0; jj < CH / 2; ++jj) {
-      uint32_t w[4];  // token g, g + 8 of piece 2 jj, then of the next
-      ldmatrix_x4(w, kt + piece_at<D>(lrow, 2 * jj + lch));
+    for (int i = 0; i < kStages; ++i) starts[i] = first_token(i, SPARSE ? listed(i) : 0);
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        uint32_t af[4];
-        codes_to_f16<CODE>(w[2 * k], af[0], af[2]);
-        codes_to_f16<CODE>(w[2 * k + 1], af[1], af[3]);
+    for (int i = 0; i < kStages - 1; ++i) fetch(i, starts[i]);
+    const int lrow = lane & 15, lch = lane >> 4;  // ldmatrix: rows 0-7, 8-15 of a piece, then of the next
+    int blk_ahead = SPARSE ? listed(kStages) : 0;
+
+    // q as the scores' B operand, its row's power of two, and what each column's rows see
+    uint32_t bq[NT][CH][2];
+    float qs[NT][2];
+    int lim[NT][2];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma_f16_16816(s[nt], af, bq[nt][2 * jj + k][0], bq[nt][2 * jj + k][1]);
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = rt * R + nt * 8 + g;
+      const uint16_t* qrow = a.q + (first + (long long)min(r, rows - 1) * step) * D;
+      uint2 raw[CH];  // four channels of every piece
+      float m = 0.0f;
+#pragma unroll
+      for (int j = 0; j < CH; ++j) {
+        raw[j] = r < rows ? *reinterpret_cast<const uint2*>(qrow + 16 * j + 4 * c) : make_uint2(0, 0);
+        m = fmaxf(m, fmaxf(fmaxf(fabsf(bf16lo(raw[j].x)), fabsf(bf16hi(raw[j].x))), fmaxf(fabsf(bf16lo(raw[j].y)), fabsf(bf16hi(raw[j].y)))));
+      }
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+      const int e = max((int)(__float_as_uint(m) >> 23) - 127, -100) - 14;  // m 2^-e in [2^14, 2^15)
+      const float up = two_to(-e);
+#pragma unroll
+      for (int j = 0; j < CH; ++j) {
+        const float v0 = bf16lo(raw[j].x) * up, v1 = bf16hi(raw[j].x) * up, v2 = bf16lo(raw[j].y) * up, v3 = bf16hi(raw[j].y) * up;
+        __half2 f0, f1;  // the order in which codes_to_f16 gives the four codes
+        if (CODE == kCache8Int8) {
+          f0 = __floats2half2_rn(v0, v2), f1 = __floats2half2_rn(v1, v3);
+        } else {
+          f0 = __floats2half2_rn(v0, v1), f1 = __floats2half2_rn(v2, v3);
+        }
+        bq[nt][j][0] = *reinterpret_cast<uint32_t*>(&f0);
+        bq[nt][j][1] = *reinterpret_cast<uint32_t*>(&f1);
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int col = 2 * c + j, rc = rt * R + nt * 8 + col;
+        qs[nt][j] = two_to(max(__shfl_sync(0xffffffffu, e, 4 * col), -126)) * (a.scale * 1.4426950408889634f);
+        const int i = SPARSE ? qi : rc % a.nq;
+        lim[nt][j] = rc < rows ? max(0, n - a.nq + 1 + i) : 0x7fffffff;  // columns beyond the rows are not stored
       }
     }
-    // s[nt][0..3]: token g (0, 1) or g + 8 (2, 3), row 2c + (index & 1)
-    bool over = false;
+
+    float o[NT][CH][4];
+    float m_run[NT][2], mv_run[NT][2], l_run[NT][2];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int t = t0 + g + 8 * (j >> 1);
-        float x = s[nt][j] * (kscale * qs[nt][j & 1]);
-        if (t0 + 16 > all_see) x = t < lim[nt][j & 1] && t < end ? x : -INFINITY;
-        s[nt][j] = x;
-        over |= x > m_run[nt][j & 1] + kLag || x + vexp > mv_run[nt][j & 1] + kLag;
+      for (int i = 0; i < CH; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[nt][i][j] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) m_run[nt][j] = mv_run[nt][j] = kNone, l_run[nt][j] = 0.0f;
+    }
+
+    for (int i = 0; i < n_mine; ++i) {
+      const int tile = tile0 + warp + i * kWarps, t0 = starts[0], st = i % kStages;
+      fetch(i + kStages - 1, starts[kStages - 1]);
+      copies_wait<kStages - 1>();
+      __syncwarp();
+#pragma unroll
+      for (int j = 0; j + 1 < kStages; ++j) starts[j] = starts[j + 1];
+      starts[kStages - 1] = first_token(i + kStages, blk_ahead);
+      if (SPARSE) blk_ahead = listed(i + kStages + 1);
+      if (SPARSE && t0 < 0) continue;  // warp-uniform
+      const uint32_t kt = ring + st * (2 * TILE), vt = kt + TILE;
+      const float kscale = s_scale[warp][st][0];
+      const float vexp = (float)((int)(__float_as_uint(s_scale[warp][st][1]) >> 23) - 127);
+
+      // scores of 16 tokens x R rows
+      float s[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.0f;
+#pragma unroll
+      for (int jj = 0; jj < CH / 2; ++jj) {
+        uint32_t w[4];  // token g, g + 8 of piece 2 jj, then of the next
+        ldmatrix_x4(w, kt + piece_at<D>(lrow, 2 * jj + lch));
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          uint32_t af[4];
+          codes_to_f16<CODE>(w[2 * k], af[0], af[2]);
+          codes_to_f16<CODE>(w[2 * k + 1], af[1], af[3]);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma_f16_16816(s[nt], af, bq[nt][2 * jj + k][0], bq[nt][2 * jj + k][1]);
+        }
       }
-    if (__any_sync(0xffffffffu, over)) {
+      // s[nt][0..3]: token g (0, 1) or g + 8 (2, 3), row 2c + (index & 1)
+      bool over = false;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const float top = column_max(fmaxf(s[nt][j], s[nt][j + 2]));
-          const float m = fmaxf(m_run[nt][j], top), mv = fmaxf(mv_run[nt][j], top + vexp);
-          const float f = ex2(m_run[nt][j] - m), fv = ex2(mv_run[nt][j] - mv);
-          m_run[nt][j] = m, mv_run[nt][j] = mv;
-          l_run[nt][j] *= f;
-#pragma unroll
-          for (int i = 0; i < D / 16; ++i) o[nt][i][j] *= fv, o[nt][i][j + 2] *= fv;
+          const float f = kscale * qs[nt][j];
+          s[nt][j] *= f, s[nt][j + 2] *= f;
+          if (t0 + 16 > all_see) {
+            const int t = t0 + g, see = min(lim[nt][j], end);
+            s[nt][j] = t < see ? s[nt][j] : -INFINITY;
+            s[nt][j + 2] = t + 8 < see ? s[nt][j + 2] : -INFINITY;
+          }
+          over |= fmaxf(s[nt][j], s[nt][j + 2]) > fminf(m_run[nt][j], mv_run[nt][j] - vexp) + kLag;
         }
-    }
-    uint32_t bhi[NT][2], blo[NT][2];
+      if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      float pv[4];
-      float tile_sum[2] = {0.0f, 0.0f};
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float p = ex2(s[nt][j] - m_run[nt][j & 1]);
-        tile_sum[j & 1] += p;
-        pv[j] = ex2(s[nt][j] + (vexp + kShift) - mv_run[nt][j & 1]);
+          for (int j = 0; j < 2; ++j) {
+            const float top = column_max(fmaxf(s[nt][j], s[nt][j + 2]));
+            const float m = fmaxf(m_run[nt][j], top), mv = fmaxf(mv_run[nt][j], top + vexp);
+            const float f = ex2(m_run[nt][j] - m), fv = ex2(mv_run[nt][j] - mv);
+            m_run[nt][j] = m, mv_run[nt][j] = mv;
+            l_run[nt][j] *= f;
+#pragma unroll
+            for (int k = 0; k < CH; ++k) o[nt][k][j] *= fv, o[nt][k][j + 2] *= fv;
+          }
       }
-      l_run[nt][0] += tile_sum[0], l_run[nt][1] += tile_sum[1];
+      uint32_t bhi[NT][2], blo[NT][2];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const __half2 hi = __floats2half2_rn(pv[2 * j], pv[2 * j + 1]);
-        const float2 back = __half22float2(hi);
-        const __half2 lo = __floats2half2_rn(pv[2 * j] - back.x, pv[2 * j + 1] - back.y);
-        bhi[nt][j] = transpose_8x8(*reinterpret_cast<const uint32_t*>(&hi));
-        blo[nt][j] = transpose_8x8(*reinterpret_cast<const uint32_t*>(&lo));
-      }
-      if (MASS) {
+      for (int nt = 0; nt < NT; ++nt) {
+        float pv[4], tile_sum[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const float sum = column_sum(tile_sum[j]);
-          const int r = rt * R + nt * 8 + 2 * c + j;
-          if (g == 0 && r < rows)
-            a.tile_mass[(first + r) * ((a.max_tokens + 15) >> 4) + tile] = make_float2(sum, m_run[nt][j]);
+          const float p0 = ex2(s[nt][j] - m_run[nt][j]), p1 = ex2(s[nt][j + 2] - m_run[nt][j]);
+          tile_sum[j] = p0 + p1;
+          l_run[nt][j] += tile_sum[j];
+          // p s_V relative to M': p 2^f <= 2^(kLag + kShift), so a factor of over 2^100 meets a p below 2^-85, whose
+          // row's sum holds a weight of 1 at least: nothing that a result in fp32 could show
+          const float f = ex2(fminf(m_run[nt][j] - mv_run[nt][j] + (vexp + kShift), 100.0f));
+          pv[j] = p0 * f, pv[j + 2] = p1 * f;
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const __half2 hi = __floats2half2_rn(pv[2 * j], pv[2 * j + 1]);
+          const float2 back = __half22float2(hi);
+          const __half2 lo = __floats2half2_rn(pv[2 * j] - back.x, pv[2 * j + 1] - back.y);
+          bhi[nt][j] = transpose_8x8(*reinterpret_cast<const uint32_t*>(&hi));
+          blo[nt][j] = transpose_8x8(*reinterpret_cast<const uint32_t*>(&lo));
+        }
+        if (MASS) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float sum = column_sum(tile_sum[j]);
+            const int r = rt * R + nt * 8 + 2 * c + j;
+            if (g == 0 && r < rows)
+              a.tile_mass[(first + r) * ((a.max_tokens + 15) >> 4) + tile] = make_float2(sum, m_run[nt][j]);
+          }
         }
       }
-    }
-    // o[channel][row] += codes^T p
+      // o[channel][row] += codes^T p
 #pragma unroll
-    for (int jj = 0; jj < CH / 2; ++jj) {
-      uint32_t w[4];  // tokens 2c, 2c + 1, then 2c + 8, 2c + 9, of channels 2g, 2g + 1 of piece 2 jj; of the next
-      ldmatrix_x4_trans(w, vt + piece_at<D>(lrow, 2 * jj + lch));
+      for (int jj = 0; jj < CH / 2; ++jj) {
+        uint32_t w[4];  // tokens 2c, 2c + 1, then 2c + 8, 2c + 9, of channels 2g, 2g + 1 of piece 2 jj; of the next
+        ldmatrix_x4_trans(w, vt + piece_at<D>(lrow, 2 * jj + lch));
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        uint32_t af[4];
-        if (CODE == kCache8E4m3) w[2 * k] = __byte_perm(w[2 * k], 0, 0x3120), w[2 * k + 1] = __byte_perm(w[2 * k + 1], 0, 0x3120);
-        codes_to_f16<CODE>(w[2 * k], af[0], af[1]);
-        codes_to_f16<CODE>(w[2 * k + 1], af[2], af[3]);
+        for (int k = 0; k < 2; ++k) {
+          uint32_t af[4];
+          if (CODE == kCache8E4m3) w[2 * k] = __byte_perm(w[2 * k], 0, 0x3120), w[2 * k + 1] = __byte_perm(w[2 * k + 1], 0, 0x3120);
+          codes_to_f16<CODE>(w[2 * k], af[0], af[1]);
+          codes_to_f16<CODE>(w[2 * k + 1], af[2], af[3]);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          mma_f16_16816(o[nt][2 * jj + k], af, bhi[nt][0], bhi[nt][1]);
-          mma_f16_16816(o[nt][2 * jj + k], af, blo[nt][0], blo[nt][1]);
+          for (int nt = 0; nt < NT; ++nt) {
+            mma_f16_16816(o[nt][2 * jj + k], af, bhi[nt][0], bhi[nt][1]);
+            mma_f16_16816(o[nt][2 * jj + k], af, blo[nt][0], blo[nt][1]);
+          }
         }
       }
+      __syncwarp();  // the stage is free for the next fetch
     }
-    __syncwarp();  // the stage is free for the next fetch
-  }
 
-  copies_wait<0>();
-  __syncthreads();  // the tiles' memory now takes the outputs
-  // merge the warps: o relative to the CTA's maxima
+    // merge the warps: o relative to the CTA's maxima
+    copies_wait<0>();
+    __syncthreads();  // the tiles' memory now takes the outputs
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const float l = column_sum(l_run[nt][j]);
-      const int r = nt * 8 + 2 * c + j;
-      if (g == 0) s_m[warp][r] = m_run[nt][j], s_mv[warp][r] = mv_run[nt][j], s_l[warp][r] = l;
+      for (int j = 0; j < 2; ++j) {
+        const float l = column_sum(l_run[nt][j]);
+        const int r = nt * 8 + 2 * c + j;
+        if (g == 0) s_m[warp][r] = m_run[nt][j], s_mv[warp][r] = mv_run[nt][j], s_l[warp][r] = l;
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i) {
-        const int ch = 16 * i + 2 * g;
-        s_o[(warp * R + r) * D + ch] = o[nt][i][j];
-        s_o[(warp * R + r) * D + ch + 1] = o[nt][i][j + 2];
+        for (int i = 0; i < CH; ++i)
+          *reinterpret_cast<float2*>(&s_o[(warp * R + r) * D + 16 * i + 2 * g]) = make_float2(o[nt][i][j], o[nt][i][j + 2]);
       }
-    }
-  __syncthreads();
-  for (int e = threadIdx.x; e < R * D; e += kWarps * 32) {
-    const int r = e / D, ch = e % D;
-    if (rt * R + r >= rows) continue;
-    float m = kNone, mv = kNone, l = 0.0f, acc = 0.0f;
+    __syncthreads();
+    const bool whole = tile0 == 0 && tile1 == tiles, ends = tile1 == tiles;
+    if (tid < R) {
+      float m = kNone, mv = kNone, l = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) m = fmaxf(m, s_m[w][r]), mv = fmaxf(mv, s_mv[w][r]);
+      for (int w = 0; w < kWarps; ++w) m = fmaxf(m, s_m[w][tid]), mv = fmaxf(mv, s_mv[w][tid]);
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      l = __fmaf_rn(s_l[w][r], ex2(s_m[w][r] - m), l);
-      acc = __fmaf_rn(s_o[(w * R + r) * D + ch], ex2(s_mv[w][r] - mv), acc);
+      for (int w = 0; w < kWarps; ++w) l = __fmaf_rn(s_l[w][tid], ex2(s_m[w][tid] - m), l);
+      const float f = !whole ? 1.0f : l > 0.0f ? ex2(mv - m - kShift) / l : 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) s_w[w][tid] = ex2(s_mv[w][tid] - mv) * f;
+      s_fin[tid][0] = m, s_fin[tid][1] = mv, s_fin[tid][2] = l;
+      if (MASS && whole && rt * R + tid < rows) a.stats[first + rt * R + tid] = make_float2(m, l > 0.0f ? 1.0f / l : 0.0f);
     }
-    const long long row = first + (rt * R + r) * step;
-    if (a.splits == 1) {
-      a.out[row * D + ch] = l > 0.0f ? acc * ex2(mv - m - kShift) / l : 0.0f;
-      if (MASS && ch == 0) a.stats[row] = make_float2(m, l > 0.0f ? 1.0f / l : 0.0f);
-    } else {
-      float* p = a.part + (row * a.splits + split) * (D + 4);
-      p[4 + ch] = acc;
-      if (ch == 0) p[0] = m, p[1] = mv, p[2] = l;
+    __syncthreads();
+    const int my_rows = min(R, rows - rt * R);
+    const long long row0 = first + (long long)rt * R * step;
+    // a unit that ends here has its last piece in slot 0, one that does not end its piece in slot 1
+    float* part = a.part + (long long)(blockIdx.x * 2 + (ends ? 0 : 1)) * R * (D + 4);
+    for (int e = tid; e < my_rows * (D / 4); e += kWarps * 32) {
+      const int r = e / (D / 4), ch = 4 * (e % (D / 4));
+      float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float4 v = *reinterpret_cast<const float4*>(&s_o[(w * R + r) * D + ch]);
+        const float f = s_w[w][r];
+        acc.x = __fmaf_rn(v.x, f, acc.x), acc.y = __fmaf_rn(v.y, f, acc.y), acc.z = __fmaf_rn(v.z, f, acc.z), acc.w = __fmaf_rn(v.w, f, acc.w);
+      }
+      float* to = whole ? a.out + (row0 + r * step) * D + ch : part + r * (D + 4) + 4 + ch;
+      *reinterpret_cast<float4*>(to) = acc;
+      if (!whole && ch == 0) *reinterpret_cast<float4*>(part + r * (D + 4)) = make_float4(s_fin[r][0], s_fin[r][1], s_fin[r][2], 0.0f);
     }
+    if (ends && !whole) {
+      tail.row0 = row0, tail.step = (int)step, tail.rows = my_rows;
+      tail.pieces = (int)(blockIdx.x - unit_at / run) + 1;
+    }
+    // the next unit
+    at += tile1 - tile0;
+    unit_at += tiles;
+    tile0 = 0;
+    if (at < end_all && ++idx == per_batch) {
+      idx = 0;
+      do {
+        if (++b == B) b = 0, ++lz;
+        tiles = unit_tiles(a, b);
+      } while (tiles == 0);
+    }
+    __syncthreads();  // the outputs' memory takes tiles again
+  }
+  if (tid == 0) reinterpret_cast<Tail*>(a.tails)[blockIdx.x] = tail;
+
+  // sequences that are empty: zeros
+  const int seq_rows = a.hq * a.nq;
+  for (long long e = blockIdx.x; e < (long long)a.nl * B; e += gridDim.x) {
+    if (unit_tiles(a, (int)(e % B))) continue;
+    float4* to = reinterpret_cast<float4*>(a.out + e * seq_rows * D);
+    for (int i = tid; i < seq_rows * (D / 4); i += kWarps * 32) to[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   }
 }
 
-// One row of the output from its splits.
+// The units whose pieces lie in several runs: piece by piece from the run in which the unit ends
+// back to the one in which it begins.  One CTA a run and row.
 template <int D>
 __global__ void __launch_bounds__(D) cache8_combine_kernel(Cache8AttnArgs a, bool mass) {
-  __shared__ float wo[kMaxSplits];
-  __shared__ float red[3][D / 32];
-  const long long row = blockIdx.x;
-  const int b = (int)(row / ((long long)a.hq * a.nq) % a.c.k.B);
-  const int live = (live_tiles(a, clamped_len(a, b)) + a.tiles_per_split - 1) / a.tiles_per_split;
-  const float* part = a.part + row * a.splits * (D + 4);
-  const int ch = threadIdx.x, warp = ch >> 5;
-  float m = kNone, mv = kNone, l = 0.0f;
-  for (int i = ch; i < live; i += D) m = fmaxf(m, part[i * (D + 4)]), mv = fmaxf(mv, part[i * (D + 4) + 1]);
-  m = warp_max_f32(m), mv = warp_max_f32(mv);
-  if ((ch & 31) == 0) red[0][warp] = m, red[1][warp] = mv;
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < D / 32; ++i) m = fmaxf(m, red[0][i]), mv = fmaxf(mv, red[1][i]);
-  for (int i = ch; i < live; i += D) {
-    l = __fmaf_rn(part[i * (D + 4) + 2], ex2(part[i * (D + 4)] - m), l);
-    wo[i] = ex2(part[i * (D + 4) + 1] - mv);
+  const int R = 8 * a.nt, ch = threadIdx.x, r = blockIdx.y;
+  dependents_may_launch();
+  previous_kernel_done();
+  const Tail tail = reinterpret_cast<const Tail*>(a.tails)[blockIdx.x];
+  if (r >= tail.rows || tail.pieces == 0) return;
+  auto piece = [&](int i) {  // 0: the last
+    return a.part + ((long long)(blockIdx.x - i) * 2 + (i ? 1 : 0)) * R * (D + 4) + r * (D + 4);
+  };
+  float m = kNone, mv = kNone, l = 0.0f, acc = 0.0f;
+  for (int i = 0; i < tail.pieces; ++i) {
+    const float4 st = *reinterpret_cast<const float4*>(piece(i));
+    const float v = piece(i)[4 + ch];
+    const float m2 = fmaxf(m, st.x), mv2 = fmaxf(mv, st.y);
+    l = l * ex2(m - m2) + st.z * ex2(st.x - m2);
+    acc = acc * ex2(mv - mv2) + v * ex2(st.y - mv2);
+    m = m2, mv = mv2;
   }
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-  if ((ch & 31) == 0) red[2][warp] = l;
-  __syncthreads();
-  l = 0.0f;
-#pragma unroll
-  for (int i = 0; i < D / 32; ++i) l += red[2][i];
-  float acc = 0.0f;
-#pragma unroll 4
-  for (int i = 0; i < live; ++i) acc = __fmaf_rn(part[i * (D + 4) + 4 + ch], wo[i], acc);
+  const long long row = tail.row0 + (long long)r * tail.step;
   a.out[row * D + ch] = l > 0.0f ? acc * ex2(mv - m - kShift) / l : 0.0f;
   if (mass && ch == 0) a.stats[row] = make_float2(m, l > 0.0f ? 1.0f / l : 0.0f);
 }
 
-// mass[block] (+)= sum over the unit's rows and the block's tiles of p
+// mass[block] (+)= sum over the unit's rows and the block's tiles of p: 32 blocks a CTA, its warps
+// take rows in turn
 __global__ void __launch_bounds__(256) cache8_mass_kernel(Cache8AttnArgs a, int chunks) {
+  __shared__ float s_sum[8][32];
   const int H = a.c.k.H, B = a.c.k.B, nb = a.c.blocks();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  dependents_may_launch();
+  previous_kernel_done();
   const long long u = blockIdx.x / chunks;
-  const int blk = (blockIdx.x % chunks) * 256 + threadIdx.x;
-  if (blk >= nb) return;
+  const int blk = (blockIdx.x % chunks) * 32 + lane;
   const int h = (int)(u % H), b = (int)((u / H) % B), lz = (int)(u / H / B);
   const int n = clamped_len(a, b), tpb = a.c.tb >> 4, tiles = (a.max_tokens + 15) >> 4, live = (n + 15) >> 4;
   const int rows = a.gq * a.nq;
-  float* at = a.mass + (((long long)(a.l0 + lz) * B + b) * H + h) * nb + blk;
+  const int i0 = blk * tpb, i1 = min(live, i0 + tpb);
   float sum = 0.0f;
-  const int i1 = min(live, (blk + 1) * tpb);
-  for (int r = 0; r < rows; ++r) {
-    const float2 st = a.stats[u * rows + r];
-    const float2* tm = a.tile_mass + (u * rows + r) * tiles;
-    float part = 0.0f;
-    for (int i = blk * tpb; i < i1; ++i) part = __fmaf_rn(tm[i].x, ex2(tm[i].y - st.x), part);
-    sum = __fmaf_rn(part, st.y, sum);
+  if (i0 < i1) {
+    for (int r = warp; r < rows; r += 8) {
+      const float2 st = a.stats[u * rows + r];
+      const float2* tm = a.tile_mass + (u * rows + r) * tiles;
+      float part = 0.0f;
+      for (int i = i0; i < i1; ++i) part = __fmaf_rn(tm[i].x, ex2(tm[i].y - st.x), part);
+      sum = __fmaf_rn(part, st.y, sum);
+    }
   }
+  s_sum[warp][lane] = sum;
+  __syncthreads();
+  if (warp || blk >= nb) return;
+#pragma unroll
+  for (int w = 1; w < 8; ++w) sum += s_sum[w][lane];
+  float* at = a.mass + (((long long)(a.l0 + lz) * B + b) * H + h) * nb + blk;
   if (!a.accumulate) {
     *at = sum;
-  } else if (blk * tpb < live) {
+  } else if (i0 < i1) {
     *at += sum;
   }
 }
@@ -436,20 +536,17 @@ namespace {
 long long total_rows(const Cache8AttnArgs& a) { return (long long)a.nl * a.c.k.B * a.hq * a.nq; }
 long long units(const Cache8AttnArgs& a) { return (long long)a.nl * a.c.k.B * a.c.k.H * (a.n_select ? a.nq : 1) * a.row_tiles; }
 
-// Rows of a CTA: 8 where they are enough, else 16 (two operand columns for one reading of the
-// codes).  Splits: as many CTAs as fill the GPU a few times over, so that ragged lengths even
-// out, but no run of fewer than 16 tiles (two a warp).
+// Rows of a unit: 8 where they are enough, else 16 (two operand columns for one reading of the
+// codes).  CTAs: as many as the GPU holds at once, but none with a run shorter than kLeastRun if
+// every sequence were of the longest length.
 void plan(Cache8AttnArgs& a) {
   const int rows = a.n_select ? a.gq : a.gq * a.nq;
   a.nt = rows > 8 ? 2 : 1;
   a.row_tiles = (rows + 8 * a.nt - 1) / (8 * a.nt);
-  const int tiles = a.n_select ? a.n_select * (a.c.tb / 16) : (a.max_tokens + 15) / 16;
-  const long long want = (8LL * kSms + units(a) - 1) / units(a);
-  long long per = (tiles + want - 1) / want;
-  per = per < 16 ? 16 : per > 64 ? 64 : per;
-  if ((tiles + per - 1) / per > kMaxSplits) per = (tiles + kMaxSplits - 1) / kMaxSplits;
-  a.tiles_per_split = (int)per;
-  a.splits = (int)((tiles + per - 1) / per);
+  const long long tiles = a.n_select ? (long long)a.n_select * (a.c.tb / 16) : (a.max_tokens + 15) / 16;
+  const long long most = kSms * (a.nt == 2 && a.c.k.d == 128 ? 1 : 2);
+  const long long runs = (units(a) * tiles + kLeastRun - 1) / kLeastRun;
+  a.ctas = (int)(runs < most ? runs : most);
 }
 
 uint64_t round16(uint64_t b) { return (b + 15) & ~15ull; }
@@ -458,14 +555,16 @@ void layout(Cache8AttnArgs& a, char* base, bool want_mass, uint64_t& bytes) {
   const uint64_t rows = (uint64_t)total_rows(a);
   uint64_t at = 0;
   a.part = reinterpret_cast<float*>(base);
-  if (a.splits > 1) at += round16(rows * a.splits * (a.c.k.d + 4) * sizeof(float));
+  at += round16((uint64_t)a.ctas * 2 * 8 * a.nt * (a.c.k.d + 4) * sizeof(float));
+  a.tails = base + at;
+  at += round16(a.ctas * sizeof(Tail));
   if (want_mass) {
     a.tile_mass = reinterpret_cast<float2*>(base + at);
     at += round16(rows * ((a.max_tokens + 15) / 16) * sizeof(float2));
     a.stats = reinterpret_cast<float2*>(base + at);
     at += round16(rows * sizeof(float2));
   }
-  bytes = at ? at : 16;
+  bytes = at;
 }
 
 template <int D, int CODE, int NT, bool SPARSE, bool MASS>
@@ -475,8 +574,7 @@ cudaError_t launch_one(const Cache8AttnArgs& a, cudaStream_t st) {
   auto kern = cache8_attn_kernel<D, CODE, NT, SPARSE, MASS>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  kern<<<(unsigned)(units(a) * a.splits), kWarps * 32, smem, st>>>(a);
-  return cudaGetLastError();
+  return launch_after(kern, dim3(a.ctas), kWarps * 32, smem, st, a);
 }
 template <int D, int CODE, int NT>
 cudaError_t launch_kind(const Cache8AttnArgs& a, cudaStream_t st) {
@@ -490,12 +588,11 @@ cudaError_t launch_d(const Cache8AttnArgs& a, cudaStream_t st) {
     e = a.nt == 1 ? launch_kind<D, kCache8Int8, 1>(a, st) : launch_kind<D, kCache8Int8, 2>(a, st);
   else
     e = a.nt == 1 ? launch_kind<D, kCache8E4m3, 1>(a, st) : launch_kind<D, kCache8E4m3, 2>(a, st);
-  if (e != cudaSuccess || a.splits == 1) return e;
-  cache8_combine_kernel<D><<<(unsigned)total_rows(a), D, 0, st>>>(a, a.mass != nullptr);
-  return cudaGetLastError();
+  if (e != cudaSuccess || a.ctas == 1) return e;
+  return launch_after(cache8_combine_kernel<D>, dim3(a.ctas, 8 * a.nt), D, 0, st, a, a.mass != nullptr);
 }
 
-int mass_chunks(const Cache8AttnArgs& a) { return (a.c.blocks() + 255) / 256; }
+int mass_chunks(const Cache8AttnArgs& a) { return (a.c.blocks() + 31) / 32; }
 
 }  // namespace
 
@@ -506,11 +603,9 @@ uint64_t cache8_attn_workspace(Cache8AttnArgs a, bool want_mass) {
   return bytes;
 }
 
-bool cache8_attn_fits(Cache8AttnArgs a) {
-  plan(a);
+bool cache8_attn_fits(const Cache8AttnArgs& a, bool want_mass) {
   const long long most = (1LL << 31) - 1;
-  return units(a) * a.splits <= most && total_rows(a) <= most &&
-         (long long)a.nl * a.c.k.B * a.c.k.H * mass_chunks(a) <= most;
+  return total_rows(a) <= most && (!want_mass || (long long)a.nl * a.c.k.B * a.c.k.H * mass_chunks(a) <= most);
 }
 
 cudaError_t launch_cache8_attention(Cache8AttnArgs a, void* workspace, cudaStream_t st) {
@@ -520,8 +615,7 @@ cudaError_t launch_cache8_attention(Cache8AttnArgs a, void* workspace, cudaStrea
   cudaError_t e = a.c.k.d == 128 ? launch_d<128>(a, st) : launch_d<64>(a, st);
   if (e != cudaSuccess || !a.mass) return e;
   const int chunks = mass_chunks(a);
-  cache8_mass_kernel<<<(unsigned)((long long)a.nl * a.c.k.B * a.c.k.H * chunks), 256, 0, st>>>(a, chunks);
-  return cudaGetLastError();
+  return launch_after(cache8_mass_kernel, dim3((unsigned)((long long)a.nl * a.c.k.B * a.c.k.H * chunks)), 256, 0, st, a, chunks);
 }
 
 }  // namespace cg

@@ -100,9 +100,10 @@ def test_attention_workspace_and_combinations():
     bad.accumulate = 2
     assert _attn(bad) == cg.CG_ERR_INVALID
     assert _attn(None) == cg.CG_ERR_INVALID
-    # a grid beyond 2^31 - 1 blocks
-    huge = cg.kv_desc(2000, 4096, 128, 32768, 128)
-    assert _attn(cg.cache8_attn_desc(128, 32768, n_layers=2000), kv=huge) == cg.CG_ERR_TOO_LARGE
+    # more than 2^31 - 1 query rows
+    huge, out = cg.kv_desc(20000, 4096, 128, 32768, 128), ctypes.c_uint64()
+    assert cg.lib().cg_cache8_attention_workspace_size(_ref(huge), _ref(C8), _ref(cg.cache8_attn_desc(128, 32768, n_layers=20000)), 0,
+                                                       ctypes.byref(out)) == cg.CG_ERR_TOO_LARGE
 
 
 def _select(sd, kv=KV, q=0x1000, scales=0x2000, bounds=0x3000, lens=0x4000, sel=0x5000, ws=0x6000, bytes_=1 << 40):
