@@ -52,7 +52,10 @@ __device__ __forceinline__ float ex2(float x) {
   return r;
 }
 // 16 bytes (or 4) from global to shared memory, asynchronously; `bytes` 0 writes zeros
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy16_or_zero(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void copy4(uint32_t dst, const void* src) {
@@ -120,6 +123,14 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 && NT == 2 ? 1 : 2) cach
   const int rows = SPARSE ? a.gq : a.gq * a.nq;
   const int per_batch = H * (SPARSE ? a.nq : 1) * a.row_tiles;  // units of one layer and sequence
   const int tb_shift = 31 - __clz(a.c.tb);
+  // where this lane's pieces stand in a tile: of its copies (32 / CH rows apart: the permutation
+  // repeats every second copy), and of its ldmatrix row (rows 0-7, 8-15 of a piece, then of the next)
+  const uint32_t ring = smem_u32(dyn) + warp * (kStages * 2 * TILE), scales_at = smem_u32(s_scale[warp]);
+  const int lane_row = lane / CH, lane_ch = lane % CH;
+  const uint32_t lane_piece[2] = {piece_at<D>(lane_row, lane_ch), piece_at<D>(lane_row + 32 / CH, lane_ch) - 512};
+  uint32_t matrix_piece[CH / 2];
+#pragma unroll
+  for (int jj = 0; jj < CH / 2; ++jj) matrix_piece[jj] = piece_at<D>(lane & 15, 2 * jj + (lane >> 4));
   dependents_may_launch();
   previous_kernel_done();
 
@@ -194,7 +205,6 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 && NT == 2 ? 1 : 2) cach
     const int end = SPARSE ? all_see : n;                          // tokens that some row sees
 
     const int* list = SPARSE ? a.sel + (u * a.nq + qi) * a.n_select : nullptr;
-    const uint32_t ring = smem_u32(dyn) + warp * (kStages * 2 * TILE);
     const int n_mine = (tile1 - tile0 - warp + kWarps - 1) / kWarps;  // this warp's tiles: tile0 + warp + i kWarps
     // the block that tile i lies in, and the tile's first token, -1 if it has none to see
     auto listed = [&](int i) { return i < n_mine ? list[((tile0 + warp + i * kWarps) * 16) >> tb_shift] : -1; };
@@ -205,19 +215,31 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 && NT == 2 ? 1 : 2) cach
       const int t0 = (blk << tb_shift) + (t & (a.c.tb - 1));
       return t0 < end ? t0 : -1;
     };
-    // codes behind the end may be anything: zeros stand for them
-    auto fetch = [&](int i, int t0) {
+    // A tile to a stage: lane pieces (row, ch), (row + 32 / CH, ch), ...  Codes behind the end may
+    // be anything: zeros stand for them.
+    const uint8_t* k_lane = kc + lane_row * D + 16 * lane_ch;
+    const uint8_t* v_lane = vc + lane_row * D + 16 * lane_ch;
+    const float* scale_lane = lane ? vs : ks;
+    auto fetch = [&](int i, int t0, int st) {
       if (i < n_mine && t0 >= 0) {
-        const uint32_t dst = ring + (i % kStages) * (2 * TILE);
+        const uint32_t dst = ring + st * (2 * TILE);
+        const long long from = (long long)t0 * D;
+        if (t0 + 16 <= end) {
 #pragma unroll
-        for (int j = 0; j < CH / 2; ++j) {
-          const int row = lane / CH + j * (32 / CH), ch = lane % CH;
-          const int bytes = t0 + row < end ? 16 : 0;
-          const long long from = (long long)(bytes ? t0 + row : t0) * D + 16 * ch;
-          copy16(dst + piece_at<D>(row, ch), kc + from, bytes);
-          copy16(dst + TILE + piece_at<D>(row, ch), vc + from, bytes);
+          for (int j = 0; j < CH / 2; ++j) {
+            copy16(dst + lane_piece[j & 1] + j * 512, k_lane + from + j * 512);
+            copy16(dst + lane_piece[j & 1] + j * 512 + TILE, v_lane + from + j * 512);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < CH / 2; ++j) {
+            const int bytes = t0 + lane_row + j * (32 / CH) < end ? 16 : 0;
+            const long long there = bytes ? from + j * 512 : from - lane_row * D;  // else a row that exists
+            copy16_or_zero(dst + lane_piece[j & 1] + j * 512, k_lane + there, bytes);
+            copy16_or_zero(dst + lane_piece[j & 1] + j * 512 + TILE, v_lane + there, bytes);
+          }
         }
-        if (lane < 2) copy4(smem_u32(&s_scale[warp][i % kStages][lane]), (lane ? vs : ks) + (t0 >> tb_shift));
+        if (lane < 2) copy4(scales_at + st * 8 + lane * 4, scale_lane + (t0 >> tb_shift));
       }
       copies_commit();
     };
@@ -225,8 +247,7 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 && NT == 2 ? 1 : 2) cach
 #pragma unroll
     for (int i = 0; i < kStages; ++i) starts[i] = first_token(i, SPARSE ? listed(i) : 0);
 #pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) fetch(i, starts[i]);
-    const int lrow = lane & 15, lch = lane >> 4;  // ldmatrix: rows 0-7, 8-15 of a piece, then of the next
+    for (int i = 0; i < kStages - 1; ++i) fetch(i, starts[i], i);
     int blk_ahead = SPARSE ? listed(kStages) : 0;
 
     // q as the scores' B operand, its row's power of two, and what each column's rows see
@@ -281,9 +302,9 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 && NT == 2 ? 1 : 2) cach
       for (int j = 0; j < 2; ++j) m_run[nt][j] = mv_run[nt][j] = kNone, l_run[nt][j] = 0.0f;
     }
 
-    for (int i = 0; i < n_mine; ++i) {
-      const int tile = tile0 + warp + i * kWarps, t0 = starts[0], st = i % kStages;
-      fetch(i + kStages - 1, starts[kStages - 1]);
+    for (int i = 0, st = 0, ahead = kStages - 1; i < n_mine; ++i, st = st + 1 == kStages ? 0 : st + 1, ahead = ahead + 1 == kStages ? 0 : ahead + 1) {
+      const int t0 = starts[0];
+      fetch(i + kStages - 1, starts[kStages - 1], ahead);
       copies_wait<kStages - 1>();
       __syncwarp();
 #pragma unroll
@@ -291,7 +312,9 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 && NT == 2 ? 1 : 2) cach
       starts[kStages - 1] = first_token(i + kStages, blk_ahead);
       if (SPARSE) blk_ahead = listed(i + kStages + 1);
       if (SPARSE && t0 < 0) continue;  // warp-uniform
-      const uint32_t kt = ring + st * (2 * TILE), vt = kt + TILE;
+      uint32_t pieces[CH / 2];  // pieces 2 jj, 2 jj + 1 of this lane's ldmatrix row
+#pragma unroll
+      for (int jj = 0; jj < CH / 2; ++jj) pieces[jj] = ring + st * (2 * TILE) + matrix_piece[jj];
       const float kscale = s_scale[warp][st][0];
       const float vexp = (float)((int)(__float_as_uint(s_scale[warp][st][1]) >> 23) - 127);
 
@@ -302,7 +325,7 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 && NT == 2 ? 1 : 2) cach
 #pragma unroll
       for (int jj = 0; jj < CH / 2; ++jj) {
         uint32_t w[4];  // token g, g + 8 of piece 2 jj, then of the next
-        ldmatrix_x4(w, kt + piece_at<D>(lrow, 2 * jj + lch));
+        ldmatrix_x4(w, pieces[jj]);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           uint32_t af[4];
@@ -369,7 +392,7 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 && NT == 2 ? 1 : 2) cach
             const float sum = column_sum(tile_sum[j]);
             const int r = rt * R + nt * 8 + 2 * c + j;
             if (g == 0 && r < rows)
-              a.tile_mass[(first + r) * ((a.max_tokens + 15) >> 4) + tile] = make_float2(sum, m_run[nt][j]);
+              a.tile_mass[(first + r) * ((a.max_tokens + 15) >> 4) + (tile0 + warp + i * kWarps)] = make_float2(sum, m_run[nt][j]);
           }
         }
       }
@@ -377,7 +400,7 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 && NT == 2 ? 1 : 2) cach
 #pragma unroll
       for (int jj = 0; jj < CH / 2; ++jj) {
         uint32_t w[4];  // tokens 2c, 2c + 1, then 2c + 8, 2c + 9, of channels 2g, 2g + 1 of piece 2 jj; of the next
-        ldmatrix_x4_trans(w, vt + piece_at<D>(lrow, 2 * jj + lch));
+        ldmatrix_x4_trans(w, pieces[jj] + TILE);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           uint32_t af[4];
