@@ -130,7 +130,11 @@ __device__ __forceinline__ float two_to(int e) { return __uint_as_float((uint32_
 template <int CODE>
 __device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
   if constexpr (CODE == kCache8Int8) {
-    const uint32_t a = (w & 0x00FF00FFu) ^ 0x64806480u, b = ((w >> 8) & 0x00FF00FFu) ^ 0x64806480u;
+    // one logic operation each: (w & m) ^ k with the mask in a register
+    uint32_t a, b, m;
+    asm("mov.b32 %0, 0x00FF00FF;" : "=r"(m));
+    asm("lop3.b32 %0, %1, %2, 0x64806480, 0x6A;" : "=r"(a) : "r"(w), "r"(m));
+    asm("lop3.b32 %0, %1, %2, 0x64806480, 0x6A;" : "=r"(b) : "r"(w >> 8), "r"(m));
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(a), "r"(0x64806480u));
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(b), "r"(0x64806480u));
   } else {

@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 && NT == 2 ? 1 : 2) cach
       }
       copies_commit();
     };
-    int starts[kStages];  // first tokens of the tiles in flight, the next one first
+    int starts[kStages];  // first tokens of the tiles in flight, by stage
 #pragma unroll
     for (int i = 0; i < kStages; ++i) starts[i] = first_token(i, SPARSE ? listed(i) : 0);
 #pragma unroll
@@ -302,15 +302,17 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 && NT == 2 ? 1 : 2) cach
       for (int j = 0; j < 2; ++j) m_run[nt][j] = mv_run[nt][j] = kNone, l_run[nt][j] = 0.0f;
     }
 
-    for (int i = 0, st = 0, ahead = kStages - 1; i < n_mine; ++i, st = st + 1 == kStages ? 0 : st + 1, ahead = ahead + 1 == kStages ? 0 : ahead + 1) {
-      const int t0 = starts[0];
-      fetch(i + kStages - 1, starts[kStages - 1], ahead);
+    for (int i0 = 0; i0 < n_mine; i0 += kStages) {
+#pragma unroll
+     for (int st = 0; st < kStages; ++st) {
+      const int i = i0 + st;
+      if (i >= n_mine) break;
+      const int t0 = starts[st], ahead = (st + kStages - 1) % kStages;
+      fetch(i + kStages - 1, starts[ahead], ahead);
+      starts[st] = first_token(i + kStages, blk_ahead);
+      if (SPARSE) blk_ahead = listed(i + kStages + 1);
       copies_wait<kStages - 1>();
       __syncwarp();
-#pragma unroll
-      for (int j = 0; j + 1 < kStages; ++j) starts[j] = starts[j + 1];
-      starts[kStages - 1] = first_token(i + kStages, blk_ahead);
-      if (SPARSE) blk_ahead = listed(i + kStages + 1);
       if (SPARSE && t0 < 0) continue;  // warp-uniform
       uint32_t pieces[CH / 2];  // pieces 2 jj, 2 jj + 1 of this lane's ldmatrix row
 #pragma unroll
@@ -415,6 +417,7 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 && NT == 2 ? 1 : 2) cach
         }
       }
       __syncwarp();  // the stage is free for the next fetch
+     }
     }
 
     // merge the warps: o relative to the CTA's maxima
