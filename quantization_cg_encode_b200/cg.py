@@ -374,32 +374,56 @@ def alloc_cache8(kvd, c8, device="cuda"):
             torch.zeros((L, B, H, nb), dtype=torch.float32, device=device))
 
 
-def _here(stream, *tensors):
-    """Stream pointer of a call whose tensors lie on the current device."""
-    dev = torch.cuda.current_device()
-    s = torch.cuda.current_stream(dev) if stream is None else stream
-    if s.device.index != dev:
-        raise ValueError("the stream is on cuda:%d, the current device is cuda:%d" % (s.device.index, dev))
-    for t in tensors:
-        if t is not None and t.is_cuda and t.get_device() != dev:
-            raise ValueError("a tensor is on cuda:%d, the current device is cuda:%d" % (t.get_device(), dev))
-    return ctypes.c_void_p(s.cuda_stream)
+def _cache8_counts(kvd, c8):
+    """What cg_cache8_sizes_for gives, without a call of the library (these calls are made once a layer
+    and token); a block size that the library refuses counts as one token."""
+    heads, T, d = kvd.layers * kvd.batch * kvd.heads, kvd.tokens, kvd.d_head
+    blocks = heads * (T // (c8.tb if c8.tb > 0 else 1))
+    return 2 * heads * T * d, 2 * blocks, 2 * blocks * d, blocks
+
+
+def _at(t, dtype, name, numel, dev):
+    """Address of a contiguous tensor of the given dtype on CUDA device `dev` (None -> NULL)."""
+    if t is None:
+        return None
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev >= 0 and t.is_contiguous() and t.numel() >= numel:
+        return t.data_ptr()
+    _ptr(t, dtype, name, numel)  # says what is wrong with it
+    raise ValueError("%s is on cuda:%d, another tensor of the call on cuda:%d" % (name, t.get_device(), dev))
+
+
+def _here(stream, dev):
+    """Stream of a call whose tensors lie on device `dev`, which has to be the current one."""
+    if dev != torch.cuda.current_device():
+        raise ValueError("the tensors are on cuda:%d, the current device is cuda:%d" % (dev, torch.cuda.current_device()))
+    if stream is None:
+        return _current_raw_stream(dev)
+    if stream.device_index != dev:
+        raise ValueError("the stream is on cuda:%d, the current device is cuda:%d" % (stream.device_index, dev))
+    return stream.cuda_stream
+
+
+# The current stream's handle without a Stream object around it, where torch has that.
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 def cg_cache8_append(kvd, c8, layer0, new, pos, counts, codes, scales, bounds, stream=None):
     """Append new bf16 [n_layers, 2, B, H, n, d] at positions pos int32 [B]; of the n tokens sequence
     b takes counts[b] (int32 [B], None: all); bounds may be None."""
-    cb, sc, bb, _ = cg_cache8_sizes_for(kvd, c8)
-    if new.dim() != 6 or tuple(new.shape[1:4]) != (2, kvd.batch, kvd.heads) or new.shape[5] != kvd.d_head:
-        raise ValueError("new must be [n_layers, 2, %d, %d, n, %d], got %s"
-                         % (kvd.batch, kvd.heads, kvd.d_head, tuple(new.shape)))
+    cb, sc, bb, _ = _cache8_counts(kvd, c8)
+    B, dev = kvd.batch, codes.get_device()
+    shape = new.shape
+    if len(shape) != 6 or shape[1] != 2 or shape[2] != B or shape[3] != kvd.heads or shape[5] != kvd.d_head:
+        raise ValueError("new must be [n_layers, 2, %d, %d, n, %d], got %s" % (B, kvd.heads, kvd.d_head, tuple(shape)))
     if new.numel() == 0:
         return
-    _check(lib().cg_cache8_append(ctypes.byref(kvd), ctypes.byref(c8), int(layer0), new.shape[0], new.shape[4],
-                                  _ptr(new, torch.bfloat16, "new"), _ptr(pos, torch.int32, "pos", kvd.batch),
-                                  _ptr(counts, torch.int32, "counts", kvd.batch), _ptr(codes, torch.uint8, "codes", cb),
-                                  _ptr(scales, torch.float32, "scales", sc), _ptr(bounds, torch.int8, "bounds", bb),
-                                  _here(stream, new, pos, counts, codes, scales, bounds)), "cg_cache8_append")
+    status = lib().cg_cache8_append(
+        ctypes.byref(kvd), ctypes.byref(c8), layer0, shape[0], shape[4], _at(new, torch.bfloat16, "new", 1, dev),
+        _at(pos, torch.int32, "pos", B, dev), _at(counts, torch.int32, "counts", B, dev),
+        _at(codes, torch.uint8, "codes", cb, dev), _at(scales, torch.float32, "scales", sc, dev),
+        _at(bounds, torch.int8, "bounds", bb, dev), _here(stream, dev))
+    _check(status, "cg_cache8_append")
 
 
 def cg_cache8_attention_workspace_size(kvd, c8, at, want_mass=False):
@@ -414,18 +438,17 @@ def cg_cache8_attention(kvd, c8, at, q, codes, scales, lens, out, workspace, sel
     """Attention of the newest q_tokens tokens over the 8-bit cache: q bf16 [n_layers, B, Hq, q_tokens, d] ->
     out fp32 of the same shape; sel int32 [n_layers, B, H, q_tokens, n_select] restricts it to listed
     blocks; mass fp32 [L, B, H, T/tb] receives every block's softmax weight."""
-    cb, sc, _, mc = cg_cache8_sizes_for(kvd, c8)
-    rows = at.n_layers * kvd.batch * at.q_tokens
+    cb, sc, _, mc = _cache8_counts(kvd, c8)
+    B, dev = kvd.batch, codes.get_device()
+    rows = at.n_layers * B * at.q_tokens
     nq = rows * at.q_heads * kvd.d_head
-    _check(lib().cg_cache8_attention(ctypes.byref(kvd), ctypes.byref(c8), ctypes.byref(at),
-                                     _ptr(q, torch.bfloat16, "q", nq), _ptr(codes, torch.uint8, "codes", cb),
-                                     _ptr(scales, torch.float32, "scales", sc),
-                                     _ptr(lens, torch.int32, "lens", kvd.batch),
-                                     _ptr(sel, torch.int32, "sel", rows * kvd.heads * at.n_select),
-                                     _ptr(out, torch.float32, "out", nq), _ptr(mass, torch.float32, "mass", mc),
-                                     _ptr(workspace, torch.uint8, "workspace"), workspace.numel(),
-                                     _here(stream, q, codes, scales, lens, sel, out, mass, workspace)),
-           "cg_cache8_attention")
+    status = lib().cg_cache8_attention(
+        ctypes.byref(kvd), ctypes.byref(c8), ctypes.byref(at), _at(q, torch.bfloat16, "q", nq, dev),
+        _at(codes, torch.uint8, "codes", cb, dev), _at(scales, torch.float32, "scales", sc, dev),
+        _at(lens, torch.int32, "lens", B, dev), _at(sel, torch.int32, "sel", rows * kvd.heads * at.n_select, dev),
+        _at(out, torch.float32, "out", nq, dev), _at(mass, torch.float32, "mass", mc, dev),
+        _at(workspace, torch.uint8, "workspace", 1, dev), workspace.numel(), _here(stream, dev))
+    _check(status, "cg_cache8_attention")
     return out
 
 
@@ -439,15 +462,16 @@ def cg_cache8_select_workspace_size(kvd, c8, sd):
 def cg_cache8_select(kvd, c8, sd, q, scales, bounds, lens, sel, workspace, stream=None):
     """The n_select blocks of each KV head and query token whose bounds promise the largest scores:
     q bf16 [n_layers, B, Hq, q_tokens, d] -> sel int32 [n_layers, B, H, q_tokens, n_select]."""
-    _, sc, bb, _ = cg_cache8_sizes_for(kvd, c8)
-    rows = sd.n_layers * kvd.batch * sd.q_tokens
-    _check(lib().cg_cache8_select(ctypes.byref(kvd), ctypes.byref(c8), ctypes.byref(sd),
-                                  _ptr(q, torch.bfloat16, "q", rows * sd.q_heads * kvd.d_head),
-                                  _ptr(scales, torch.float32, "scales", sc), _ptr(bounds, torch.int8, "bounds", bb),
-                                  _ptr(lens, torch.int32, "lens", kvd.batch),
-                                  _ptr(sel, torch.int32, "sel", rows * kvd.heads * sd.n_select),
-                                  _ptr(workspace, torch.uint8, "workspace"), workspace.numel(),
-                                  _here(stream, q, scales, bounds, lens, sel, workspace)), "cg_cache8_select")
+    _, sc, bb, _ = _cache8_counts(kvd, c8)
+    B, dev = kvd.batch, bounds.get_device()
+    rows = sd.n_layers * B * sd.q_tokens
+    status = lib().cg_cache8_select(
+        ctypes.byref(kvd), ctypes.byref(c8), ctypes.byref(sd),
+        _at(q, torch.bfloat16, "q", rows * sd.q_heads * kvd.d_head, dev), _at(scales, torch.float32, "scales", sc, dev),
+        _at(bounds, torch.int8, "bounds", bb, dev), _at(lens, torch.int32, "lens", B, dev),
+        _at(sel, torch.int32, "sel", rows * kvd.heads * sd.n_select, dev), _at(workspace, torch.uint8, "workspace", 1, dev),
+        workspace.numel(), _here(stream, dev))
+    _check(status, "cg_cache8_select")
     return sel
 
 
@@ -455,20 +479,18 @@ def cg_cache8_evict(kvd, c8, ev, lens, codes, scales, bounds, mass, to_kvd, to_c
                     to_lens, kept, stream=None):
     """Move the blocks with the largest attention weight to another cache (bounds and to_bounds may
     both be None); kept int32 [n_layers, B, H, keep_blocks] receives their indices."""
-    cb, sc, bb, mc = cg_cache8_sizes_for(kvd, c8)
-    tcb, tsc, tbb, tmc = cg_cache8_sizes_for(to_kvd, c8)
-    _check(lib().cg_cache8_evict(ctypes.byref(kvd), ctypes.byref(c8), ctypes.byref(ev),
-                                 _ptr(lens, torch.int32, "lens", kvd.batch), _ptr(codes, torch.uint8, "codes", cb),
-                                 _ptr(scales, torch.float32, "scales", sc), _ptr(bounds, torch.int8, "bounds", bb),
-                                 _ptr(mass, torch.float32, "mass", mc), ctypes.byref(to_kvd),
-                                 _ptr(to_codes, torch.uint8, "to_codes", tcb),
-                                 _ptr(to_scales, torch.float32, "to_scales", tsc),
-                                 _ptr(to_bounds, torch.int8, "to_bounds", tbb),
-                                 _ptr(to_mass, torch.float32, "to_mass", tmc),
-                                 _ptr(to_lens, torch.int32, "to_lens", kvd.batch),
-                                 _ptr(kept, torch.int32, "kept", ev.n_layers * kvd.batch * kvd.heads * ev.keep_blocks),
-                                 _here(stream, lens, codes, scales, bounds, mass, to_codes, to_scales, to_bounds,
-                                       to_mass, to_lens, kept)), "cg_cache8_evict")
+    cb, sc, bb, mc = _cache8_counts(kvd, c8)
+    tcb, tsc, tbb, tmc = _cache8_counts(to_kvd, c8)
+    B, dev = kvd.batch, codes.get_device()
+    status = lib().cg_cache8_evict(
+        ctypes.byref(kvd), ctypes.byref(c8), ctypes.byref(ev), _at(lens, torch.int32, "lens", B, dev),
+        _at(codes, torch.uint8, "codes", cb, dev), _at(scales, torch.float32, "scales", sc, dev),
+        _at(bounds, torch.int8, "bounds", bb, dev), _at(mass, torch.float32, "mass", mc, dev), ctypes.byref(to_kvd),
+        _at(to_codes, torch.uint8, "to_codes", tcb, dev), _at(to_scales, torch.float32, "to_scales", tsc, dev),
+        _at(to_bounds, torch.int8, "to_bounds", tbb, dev), _at(to_mass, torch.float32, "to_mass", tmc, dev),
+        _at(to_lens, torch.int32, "to_lens", B, dev),
+        _at(kept, torch.int32, "kept", ev.n_layers * B * kvd.heads * ev.keep_blocks, dev), _here(stream, dev))
+    _check(status, "cg_cache8_evict")
 
 
 def cg_spectral_workspace_size(kvd, st, want_grad):

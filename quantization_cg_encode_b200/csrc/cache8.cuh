@@ -7,6 +7,8 @@
 //        block: int8 codes as they are, e4m3 codes in units of 448 / 127 rounded outwards
 // mass   fp32 [L][B][H][T/tb]    the attention weight that the block has drawn
 #pragma once
+#include <atomic>
+
 #include "cg_kernels.cuh"
 
 namespace cg {
@@ -51,13 +53,14 @@ struct Cache8AttnArgs {
   // set by the launcher
   int nt;                  // query rows of a CTA / 8
   int row_tiles, ctas;
+  int cluster;             // CTAs that share one unit, 0: every CTA takes an equal run of all tiles
   float* part;             // [cta][2][8 nt][d + 4] {max, max with value scale, sum, -, o[d]}
   void* tails;             // [cta]
   float2* tile_mass;       // [row][16-token tile] {sum, its reference}
   float2* stats;           // [row] {max, 1 / sum}
 };
 uint64_t cache8_attn_workspace(Cache8AttnArgs a, bool want_mass);
-bool cache8_attn_fits(const Cache8AttnArgs& a, bool want_mass);
+bool cache8_attn_fits(Cache8AttnArgs a, bool want_mass);
 cudaError_t launch_cache8_attention(Cache8AttnArgs a, void* workspace, cudaStream_t st);
 
 struct Cache8SelectArgs {
@@ -94,20 +97,35 @@ struct Cache8EvictArgs {
 bool cache8_evict_fits(const Cache8EvictArgs& a);
 cudaError_t launch_cache8_evict(const Cache8EvictArgs& a, cudaStream_t st);
 
+// Lets a kernel use `bytes` of dynamic shared memory, once for each device
+inline cudaError_t allow_smem(const void* kern, size_t bytes, std::atomic<uint64_t>& ready) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (dev < 64 && (ready.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess) ready.fetch_or(bit, std::memory_order_release);
+  return e;
+}
+
 // Launch that may begin while the kernel before it on the stream still runs; such a kernel calls
-// previous_kernel_done() in every thread before it touches memory.
+// previous_kernel_done() in every thread before it touches memory.  `cluster` CTAs form a cluster.
 template <typename... P, typename... A>
-cudaError_t launch_after(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, A... args) {
+cudaError_t launch_after(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, int cluster, A... args) {
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr = {};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchAttribute attr[2] = {};
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster > 1 ? cluster : 1;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, P(args)...);
 }
 __device__ __forceinline__ void previous_kernel_done() { asm volatile("griddepcontrol.wait;" ::: "memory"); }

@@ -26,7 +26,10 @@
 // lengths and odd head counts leave no CTA waiting.  Within a run a warp fetches its tiles by
 // itself (cp.async, a ring of kStages tiles); at a unit's end the warps merge in shared memory.
 // A unit that lies in one run goes out as it is; the pieces of the others go to the workspace
-// and a second kernel merges them.
+// and a second kernel merges them.  Where units are few and short, a cluster of CTAs takes each
+// instead and merges through its shared memory: no looking for a place, no second kernel.
+#include <cooperative_groups.h>
+
 #include "cache8.cuh"
 
 namespace cg {
@@ -37,6 +40,8 @@ constexpr int kWarps = 8;
 constexpr int kStages = 3;
 constexpr int kSms = 148;               // what the number of CTAs is sized for
 constexpr int kLeastRun = kWarps;       // tiles: one a warp
+constexpr int kMaxCluster = 8;
+constexpr int kClusterTiles = 6;        // tiles that a warp takes in about the time of a second kernel
 constexpr float kNone = -1.0e30f;       // a running maximum that has seen nothing
 constexpr float kLag = 8.0f;            // how far a value may lie above the running maximum
 constexpr float kShift = 7.0f;          // 2^kShift p' <= 2^15 fits fp16
@@ -113,11 +118,10 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 && NT == 2 ? 1 : 2) cach
   __shared__ float s_m[kWarps][R], s_mv[kWarps][R], s_l[kWarps][R];
   __shared__ float s_w[kWarps][R], s_fin[R][3];
   __shared__ float s_scale[kWarps][kStages][2];
-  __shared__ long long s_sum[kWarps], s_before;
-  __shared__ int s_batch;
   // the warps' tiles [kWarps][kStages][key, value][TILE], then their outputs fp32 [kWarps][R][D]
   extern __shared__ __align__(128) unsigned char dyn[];
   float* s_o = reinterpret_cast<float*>(dyn);
+  float* s_part = s_o + kWarps * R * D;  // [R][D + 4]: the CTA's piece of its cluster's unit
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
   const int H = a.c.k.H, B = a.c.k.B;
   const int rows = SPARSE ? a.gq : a.gq * a.nq;
@@ -134,65 +138,66 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 && NT == 2 ? 1 : 2) cach
   dependents_may_launch();
   previous_kernel_done();
 
-  // Tiles of one layer: the sum over the batch, 256 sequences at a time; with it the run of this
-  // CTA and the sequence in which it begins.
-  auto block_scan = [&](long long v, long long& total) {  // exclusive prefix over the CTA
-    long long incl = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long x = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += x;
-    }
-    __syncthreads();
-    if (lane == 31) s_sum[warp] = incl;
-    __syncthreads();
-    long long before = 0;
-    total = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) before += s_sum[w];
-      total += s_sum[w];
-    }
-    return before + incl - v;
-  };
-  long long layer_tiles = 0;
-  for (int b0 = 0; b0 < B; b0 += kWarps * 32) {
-    long long t;
-    block_scan(b0 + tid < B ? (long long)unit_tiles(a, b0 + tid) * per_batch : 0, t);
-    layer_tiles += t;
-  }
-  const long long total = layer_tiles * a.nl;
-  const long long run = max((long long)kLeastRun, (total + gridDim.x - 1) / gridDim.x);
-  const long long begin = min(total, blockIdx.x * run), end_all = min(total, begin + run);
   int lz = 0, b = 0, idx = 0, tile0 = 0, tiles = 0;
-  long long unit_at = 0;  // the unit's first tile in the row of all tiles
-  if (begin < end_all) {
-    lz = (int)(begin / layer_tiles);
-    const long long rem = begin - lz * layer_tiles;
-    long long passed = 0;
-    for (int b0 = 0; b0 < B; b0 += kWarps * 32) {
-      const long long v = b0 + tid < B ? (long long)unit_tiles(a, b0 + tid) * per_batch : 0;
-      long long t;
-      const long long before = passed + block_scan(v, t);
-      if (before <= rem && rem < before + v) s_batch = b0 + tid, s_before = before;
-      passed += t;
-    }
-    __syncthreads();
-    b = s_batch;
+  int unit_at = 0;  // the unit's first tile in the row of all tiles
+  int begin = 0, end_all, run = 1;
+  if (a.cluster) {  // a cluster is a unit: an equal part of its tiles to every CTA
+    const int unit = blockIdx.x / a.cluster, rank = blockIdx.x % a.cluster;
+    idx = unit % per_batch, b = unit / per_batch % B, lz = unit / per_batch / B;
     tiles = unit_tiles(a, b);
-    idx = (int)((rem - s_before) / tiles);
-    unit_at = lz * layer_tiles + s_before + (long long)idx * tiles;
-    tile0 = (int)(begin - unit_at);
+    const int part = (tiles + a.cluster - 1) / a.cluster;
+    begin = tile0 = min(tiles, rank * part);
+    end_all = min(tiles, begin + part);
+    float* mine = s_part;
+    if (begin == end_all && a.cluster > 1)  // a piece without weight
+      for (int e = tid; e < R * (D + 4); e += kWarps * 32) mine[e] = e % (D + 4) < 2 ? kNone : 0.0f;
+  } else {
+    // The run of this CTA in the row of all tiles, and the unit in which it begins: every warp sums
+    // the batch's tiles for itself, 32 sequences at a time, and finds the place on a second way.
+    int batch_tiles = 0;  // of one unit of every sequence
+    for (int b0 = lane; b0 < B; b0 += 32) batch_tiles += unit_tiles(a, b0);
+    batch_tiles = __reduce_add_sync(0xffffffffu, batch_tiles);
+    const int layer_tiles = batch_tiles * per_batch, total = layer_tiles * a.nl;
+    run = max(kLeastRun, (total + (int)gridDim.x - 1) / (int)gridDim.x);
+    begin = (int)min((long long)total, (long long)blockIdx.x * run);
+    end_all = min(total, begin + run);
+    const bool any = begin < end_all;
+    lz = any ? begin / layer_tiles : 0;
+    const int rem = begin - lz * layer_tiles;
+    int passed = 0;
+    for (int b0 = 0; any; b0 += 32) {
+      const int v = b0 + lane < B ? unit_tiles(a, b0 + lane) * per_batch : 0;
+      int incl = v;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += x;
+      }
+      const unsigned in = __ballot_sync(0xffffffffu, rem < passed + incl);
+      if (in) {
+        const int first = __ffs(in) - 1;  // the first sequence whose tiles end behind the place
+        b = b0 + first;
+        tiles = __shfl_sync(0xffffffffu, v, first) / per_batch;
+        passed += __shfl_sync(0xffffffffu, incl - v, first);
+        break;
+      }
+      passed += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (any) {
+      idx = (rem - passed) / tiles;
+      unit_at = lz * layer_tiles + passed + idx * tiles;
+      tile0 = begin - unit_at;
+    }
   }
 
   Tail tail = {0, 0, 0, 0, 0};
-  for (long long at = begin; at < end_all;) {
+  for (int at = begin; at < end_all;) {
     const int rt = idx % a.row_tiles;
     const int qi = SPARSE ? idx / a.row_tiles % a.nq : 0;  // the query token of a sparse unit
     const int h = idx / a.row_tiles / (SPARSE ? a.nq : 1);
     const long long u = ((long long)lz * B + b) * H + h;
     const int n = clamped_len(a, b);
-    const int tile1 = (int)min((long long)tiles, tile0 + (end_all - at));
+    const int tile1 = min(tiles, tile0 + (end_all - at));
     // row r of the unit is row `first + r step` of the [nl][B][hq][nq] rows
     const long long first = u * a.gq * a.nq + qi, step = SPARSE ? a.nq : 1;
     const long long ks_slice = (((long long)(a.l0 + lz) * 2 + 0) * B + b) * H + h;
@@ -435,7 +440,7 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 && NT == 2 ? 1 : 2) cach
           *reinterpret_cast<float2*>(&s_o[(warp * R + r) * D + 16 * i + 2 * g]) = make_float2(o[nt][i][j], o[nt][i][j + 2]);
       }
     __syncthreads();
-    const bool whole = tile0 == 0 && tile1 == tiles, ends = tile1 == tiles;
+    const bool ends = tile1 == tiles, whole = ends && tile0 == 0 && a.cluster <= 1;
     if (tid < R) {
       float m = kNone, mv = kNone, l = 0.0f;
 #pragma unroll
@@ -452,7 +457,7 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 && NT == 2 ? 1 : 2) cach
     const int my_rows = min(R, rows - rt * R);
     const long long row0 = first + (long long)rt * R * step;
     // a unit that ends here has its last piece in slot 0, one that does not end its piece in slot 1
-    float* part = a.part + (long long)(blockIdx.x * 2 + (ends ? 0 : 1)) * R * (D + 4);
+    float* part = a.cluster ? s_part : a.part + (long long)(blockIdx.x * 2 + (ends ? 0 : 1)) * R * (D + 4);
     for (int e = tid; e < my_rows * (D / 4); e += kWarps * 32) {
       const int r = e / (D / 4), ch = 4 * (e % (D / 4));
       float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -468,7 +473,7 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 && NT == 2 ? 1 : 2) cach
     }
     if (ends && !whole) {
       tail.row0 = row0, tail.step = (int)step, tail.rows = my_rows;
-      tail.pieces = (int)(blockIdx.x - unit_at / run) + 1;
+      tail.pieces = (int)blockIdx.x - unit_at / run + 1;
     }
     // the next unit
     at += tile1 - tile0;
@@ -483,7 +488,38 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 && NT == 2 ? 1 : 2) cach
     }
     __syncthreads();  // the outputs' memory takes tiles again
   }
-  if (tid == 0) reinterpret_cast<Tail*>(a.tails)[blockIdx.x] = tail;
+  if (a.cluster > 1) {
+    namespace cgs = cooperative_groups;
+    cgs::cluster_group cluster = cgs::this_cluster();
+    cluster.sync();
+    if (tiles) {  // the rows in turn, a warp each
+      const int unit = blockIdx.x / a.cluster, rank = blockIdx.x % a.cluster;
+      const int at = unit % per_batch, rt = at % a.row_tiles, qi = SPARSE ? at / a.row_tiles % a.nq : 0;
+      const long long u = ((long long)lz * B + b) * H + at / a.row_tiles / (SPARSE ? a.nq : 1);
+      const long long first = u * a.gq * a.nq + qi, step = SPARSE ? a.nq : 1;
+      for (int r = rank * kWarps + warp; r < min(R, rows - rt * R); r += a.cluster * kWarps) {
+        float m = kNone, mv = kNone, l = 0.0f, acc[D / 32];
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) acc[j] = 0.0f;
+        for (int i = 0; i < a.cluster; ++i) {
+          const float* p = cluster.map_shared_rank(s_part, i) + r * (D + 4);
+          const float4 st = *reinterpret_cast<const float4*>(p);
+          const float m2 = fmaxf(m, st.x), mv2 = fmaxf(mv, st.y), f = ex2(mv - mv2), fi = ex2(st.y - mv2);
+          l = l * ex2(m - m2) + st.z * ex2(st.x - m2);
+#pragma unroll
+          for (int j = 0; j < D / 32; ++j) acc[j] = acc[j] * f + p[4 + 32 * j + lane] * fi;
+          m = m2, mv = mv2;
+        }
+        const long long row = first + (long long)(rt * R + r) * step;
+        const float f = l > 0.0f ? ex2(mv - m - kShift) / l : 0.0f;
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) a.out[row * D + 32 * j + lane] = acc[j] * f;
+        if (MASS && lane == 0) a.stats[row] = make_float2(m, l > 0.0f ? 1.0f / l : 0.0f);
+      }
+    }
+    cluster.sync();  // no CTA ends while another reads its piece
+  }
+  if (tid == 0 && !a.cluster) reinterpret_cast<Tail*>(a.tails)[blockIdx.x] = tail;
 
   // sequences that are empty: zeros
   const int seq_rows = a.hq * a.nq;
@@ -562,6 +598,12 @@ namespace {
 long long total_rows(const Cache8AttnArgs& a) { return (long long)a.nl * a.c.k.B * a.hq * a.nq; }
 long long units(const Cache8AttnArgs& a) { return (long long)a.nl * a.c.k.B * a.c.k.H * (a.n_select ? a.nq : 1) * a.row_tiles; }
 
+// tiles of the call if every sequence had the longest length
+long long tiles_of(const Cache8AttnArgs& a) {
+  const double u = (double)units(a), t = a.n_select ? (double)a.n_select * (a.c.tb / 16) : (double)((a.max_tokens + 15) / 16);
+  return u * t < 9.0e18 ? units(a) * (long long)t : 1LL << 62;
+}
+
 // Rows of a unit: 8 where they are enough, else 16 (two operand columns for one reading of the
 // codes).  CTAs: as many as the GPU holds at once, but none with a run shorter than kLeastRun if
 // every sequence were of the longest length.
@@ -569,10 +611,16 @@ void plan(Cache8AttnArgs& a) {
   const int rows = a.n_select ? a.gq : a.gq * a.nq;
   a.nt = rows > 8 ? 2 : 1;
   a.row_tiles = (rows + 8 * a.nt - 1) / (8 * a.nt);
-  const long long tiles = a.n_select ? (long long)a.n_select * (a.c.tb / 16) : (a.max_tokens + 15) / 16;
   const long long most = kSms * (a.nt == 2 && a.c.k.d == 128 ? 1 : 2);
-  const long long runs = (units(a) * tiles + kLeastRun - 1) / kLeastRun;
+  const long long runs = (tiles_of(a) + kLeastRun - 1) / kLeastRun;
   a.ctas = (int)(runs < most ? runs : most);
+  // clusters: as many CTAs as give each warp one tile of the longest unit, where the GPU holds them
+  // all at once and no warp gets more than kClusterTiles
+  const long long unit = a.n_select ? (long long)a.n_select * (a.c.tb / 16) : (a.max_tokens + 15) / 16;
+  int size = 1;
+  while (size < kMaxCluster && size * kWarps < unit && units(a) * size * 2 <= most) size *= 2;
+  a.cluster = units(a) <= most && unit <= (long long)size * kWarps * kClusterTiles ? size : 0;
+  if (a.cluster) a.ctas = (int)units(a) * size;
 }
 
 uint64_t round16(uint64_t b) { return (b + 15) & ~15ull; }
@@ -595,12 +643,13 @@ void layout(Cache8AttnArgs& a, char* base, bool want_mass, uint64_t& bytes) {
 
 template <int D, int CODE, int NT, bool SPARSE, bool MASS>
 cudaError_t launch_one(const Cache8AttnArgs& a, cudaStream_t st) {
-  const size_t tiles = (size_t)kWarps * kStages * 32 * D, outputs = sizeof(float) * kWarps * 8 * NT * D;
+  const size_t tiles = (size_t)kWarps * kStages * 32 * D, outputs = sizeof(float) * 8 * NT * (kWarps * D + D + 4);
   const size_t smem = tiles > outputs ? tiles : outputs;
   auto kern = cache8_attn_kernel<D, CODE, NT, SPARSE, MASS>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static std::atomic<uint64_t> ready{0};  // a bit a device
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), smem, ready);
   if (e != cudaSuccess) return e;
-  return launch_after(kern, dim3(a.ctas), kWarps * 32, smem, st, a);
+  return launch_after(kern, dim3(a.ctas), kWarps * 32, smem, st, a.cluster, a);
 }
 template <int D, int CODE, int NT>
 cudaError_t launch_kind(const Cache8AttnArgs& a, cudaStream_t st) {
@@ -614,8 +663,8 @@ cudaError_t launch_d(const Cache8AttnArgs& a, cudaStream_t st) {
     e = a.nt == 1 ? launch_kind<D, kCache8Int8, 1>(a, st) : launch_kind<D, kCache8Int8, 2>(a, st);
   else
     e = a.nt == 1 ? launch_kind<D, kCache8E4m3, 1>(a, st) : launch_kind<D, kCache8E4m3, 2>(a, st);
-  if (e != cudaSuccess || a.ctas == 1) return e;
-  return launch_after(cache8_combine_kernel<D>, dim3(a.ctas, 8 * a.nt), D, 0, st, a, a.mass != nullptr);
+  if (e != cudaSuccess || a.cluster) return e;
+  return launch_after(cache8_combine_kernel<D>, dim3(a.ctas, 8 * a.nt), D, 0, st, 1, a, a.mass != nullptr);
 }
 
 int mass_chunks(const Cache8AttnArgs& a) { return (a.c.blocks() + 31) / 32; }
@@ -629,9 +678,10 @@ uint64_t cache8_attn_workspace(Cache8AttnArgs a, bool want_mass) {
   return bytes;
 }
 
-bool cache8_attn_fits(const Cache8AttnArgs& a, bool want_mass) {
+bool cache8_attn_fits(Cache8AttnArgs a, bool want_mass) {
   const long long most = (1LL << 31) - 1;
-  return total_rows(a) <= most && (!want_mass || (long long)a.nl * a.c.k.B * a.c.k.H * mass_chunks(a) <= most);
+  plan(a);
+  return tiles_of(a) <= most && total_rows(a) <= most && (!want_mass || (long long)a.nl * a.c.k.B * a.c.k.H * mass_chunks(a) <= most);
 }
 
 cudaError_t launch_cache8_attention(Cache8AttnArgs a, void* workspace, cudaStream_t st) {
@@ -641,7 +691,7 @@ cudaError_t launch_cache8_attention(Cache8AttnArgs a, void* workspace, cudaStrea
   cudaError_t e = a.c.k.d == 128 ? launch_d<128>(a, st) : launch_d<64>(a, st);
   if (e != cudaSuccess || !a.mass) return e;
   const int chunks = mass_chunks(a);
-  return launch_after(cache8_mass_kernel, dim3((unsigned)((long long)a.nl * a.c.k.B * a.c.k.H * chunks)), 256, 0, st, a, chunks);
+  return launch_after(cache8_mass_kernel, dim3((unsigned)((long long)a.nl * a.c.k.B * a.c.k.H * chunks)), 256, 0, st, 1, a, chunks);
 }
 
 }  // namespace cg
