@@ -7,10 +7,11 @@
 // rounding of an exact number, so the codes do not depend on how the arithmetic is done, and an
 // e4m3 code loses nothing unless it falls below the normal range.
 //
-// Memory bound: 2 bytes read and 1 written a value.  One CTA takes 64 tokens of one or more
-// blocks, a warp 16 of them, which it holds in registers between the maximum and the rounding,
-// so that the input is read once; a lane has the same four channels of every token, so that the
-// per-channel bounds need no exchange within a warp (d = 128).
+// Memory bound: 2 bytes read and 1 written a value.  A warp takes 16 tokens, which it holds in
+// registers between the maximum and the rounding, so that the input is read once (16-byte loads,
+// eight in flight); a lane has the same eight channels of every second (fourth) token, so the
+// extremes of its channels are packed bf16 operations on the input as it is, and everything else
+// that needs them, the block's maximum and the bounds, comes from those: the rounding keeps order.
 #include "cache8.cuh"
 
 namespace cg {
@@ -19,21 +20,22 @@ namespace {
 
 constexpr int kWarps = 4;
 
-__device__ __forceinline__ uint32_t pack_codes_i8(float a, float b, float c, float d) {
-  const uint32_t ia = (uint32_t)__float2int_rn(a) & 255u, ib = (uint32_t)__float2int_rn(b) & 255u;
-  const uint32_t ic = (uint32_t)__float2int_rn(c) & 255u, id = (uint32_t)__float2int_rn(d) & 255u;
-  return ia | (ib << 8) | (ic << 16) | (id << 24);
-}
-__device__ __forceinline__ uint32_t pack_codes_e4m3(float a, float b, float c, float d) {
-  uint32_t r;
-  asm("{\n .reg .b16 l, h;\n cvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n cvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n mov.b32 %0, {l, h};\n}\n"
-      : "=r"(r)
-      : "f"(a), "f"(b), "f"(c), "f"(d));
-  return r;
-}
+// c = rnd(v) of four values as bytes.  int8: 1.5 2^23 + v is rounded to a whole number, whose low
+// byte is the code.
 template <int CODE>
-__device__ __forceinline__ uint32_t pack_codes(const float (&v)[4]) {
-  return CODE == kCache8Int8 ? pack_codes_i8(v[0], v[1], v[2], v[3]) : pack_codes_e4m3(v[0], v[1], v[2], v[3]);
+__device__ __forceinline__ uint32_t pack_codes(float a, float b, float c, float d) {
+  if constexpr (CODE == kCache8Int8) {
+    const float k = 12582912.0f;
+    const uint32_t ab = __byte_perm(__float_as_uint(a + k), __float_as_uint(b + k), 0x0040);
+    const uint32_t cd = __byte_perm(__float_as_uint(c + k), __float_as_uint(d + k), 0x0040);
+    return __byte_perm(ab, cd, 0x5410);
+  } else {
+    uint32_t r;
+    asm("{\n .reg .b16 l, h;\n cvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n cvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n mov.b32 %0, {l, h};\n}\n"
+        : "=r"(r)
+        : "f"(a), "f"(b), "f"(c), "f"(d));
+    return r;
+  }
 }
 template <int CODE>
 __device__ __forceinline__ void unpack_codes(uint32_t w, float (&v)[4]) {
@@ -47,8 +49,8 @@ __device__ __forceinline__ void unpack_codes(uint32_t w, float (&v)[4]) {
     v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
   }
 }
-// Bounds of four channels as int8.  e4m3 values are multiples of 2^-9, so the quotient by
-// 448 / 127 is rounded outwards in whole numbers.
+// Bounds of a channel from its least and largest code value.  e4m3 values are multiples of 2^-9,
+// so the quotient by 448 / 127 is rounded outwards in whole numbers.
 __device__ __forceinline__ int floor_div(int a, int b) {
   const int q = a / b;
   return q - (a % b < 0);
@@ -61,133 +63,177 @@ template <int CODE>
 __device__ __forceinline__ int high_bound(float v) {
   return CODE == kCache8Int8 ? (int)v : -floor_div((int)(-v * 512.0f) * 127, 448 * 512);
 }
+__device__ __forceinline__ __nv_bfloat162 as_bf16x2(uint32_t w) { return *reinterpret_cast<__nv_bfloat162*>(&w); }
+__device__ __forceinline__ uint32_t as_u32(__nv_bfloat162 v) { return *reinterpret_cast<uint32_t*>(&v); }
+constexpr uint32_t kBf16Inf2 = 0x7F807F80u, kBf16NegInf2 = 0xFF80FF80u;
 
 template <int D, int CODE>
 __global__ void __launch_bounds__(kWarps * 32) append_kernel(Cache8AppendArgs a) {
-  constexpr int LPT = D / 4;         // lanes a token
-  constexpr int TPL = 32 / LPT;      // tokens a warp loads at once
+  constexpr int LPT = D / 8;         // lanes a token
+  constexpr int TPL = 32 / LPT;      // tokens a warp loads at once: 2 or 4
   constexpr int NL = 16 / TPL;       // loads of a warp
   __shared__ float s_max[kWarps];
-  __shared__ float s_lo[kWarps][D], s_hi[kWarps][D];
+  __shared__ float s_lo[kWarps][D], s_hi[kWarps][D];  // extremes of the code values
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tb = a.c.tb, wpb = tb >> 4;               // warps of a block: 1, 2 or 4
   const int window = (a.n + tb - 2) / tb + 1;         // blocks that n tokens touch at most
-  const long long slices = (long long)a.nl * 2 * a.c.k.B * a.c.k.H;
-  const long long item = (long long)blockIdx.x * (kWarps / wpb) + warp / wpb;  // (slice, block of the window)
+  const int items = a.nl * 2 * a.c.k.B * a.c.k.H * window;
+  const int item = blockIdx.x * (kWarps / wpb) + warp / wpb;  // (slice, block of the window)
   const int part = warp % wpb;
-  const bool inside = item < slices * window;
-  const long long sl = inside ? item / window : 0;
-  const int w = inside ? (int)(item % window) : 0;
-  int h, b, s, lz;
-  {
-    long long r = sl;
-    h = (int)(r % a.c.k.H), r /= a.c.k.H;
-    b = (int)(r % a.c.k.B), r /= a.c.k.B;
-    s = (int)(r & 1), lz = (int)(r >> 1);
-  }
+  const bool inside = item < items;
+  const int sl = inside ? item / window : 0, w = inside ? item % window : 0;
+  const int h = sl % a.c.k.H, b = sl / a.c.k.H % a.c.k.B, s = sl / a.c.k.H / a.c.k.B & 1, lz = sl / a.c.k.H / a.c.k.B >> 1;
+  previous_kernel_done();
   const int pos = a.pos[b];
   const int cnt = min(a.n, a.counts ? a.counts[b] : a.n);
   // tokens [pos, end) are new; positions off the cache are not written
-  const long long end = pos < 0 || cnt <= 0 ? 0 : min((long long)pos + cnt, (long long)a.c.k.T);
-  const int blk = inside && pos >= 0 ? pos / tb + w : 0;
-  const long long b0 = (long long)blk * tb;
+  const int end = pos < 0 || cnt <= 0 ? 0 : (int)min((long long)pos + cnt, (long long)a.c.k.T);
+  const long long b0 = pos < 0 ? 0 : ((long long)(pos / tb) + w) * tb;  // the block's first token
   const bool live = inside && pos >= 0 && b0 < end;
-  bool has_old = live && b0 < pos;
+  if (__syncthreads_or(live) == 0) return;
+  const int blk = live ? (int)(b0 / tb) : 0;
   const long long slice = (((long long)(a.l0 + lz) * 2 + s) * a.c.k.B + b) * a.c.k.H + h;
 
-  const int ch = 4 * (lane % LPT), sub = lane / LPT;  // channels [ch, ch + 4), token of the pair
-  const int t0 = (int)b0 + 16 * part + sub;
-  uint2 x[NL];
-  float m = 0.0f;
+  const int ch = 8 * (lane % LPT), sub = lane / LPT;  // channels [ch, ch + 8), token of the load
+  const int t0 = (live ? (int)b0 : 0) + 16 * part + sub;
+  uint4 x[NL];
 #pragma unroll
   for (int i = 0; i < NL; ++i) {
     const int t = t0 + i * TPL;
-    x[i] = make_uint2(0, 0);
-    if (live && t >= pos && t < end)
-      x[i] = *reinterpret_cast<const uint2*>(a.x + (sl * a.n + (t - pos)) * D + ch);
+    x[i] = make_uint4(0, 0, 0, 0);
+    if (live && t >= pos && t < end) x[i] = *reinterpret_cast<const uint4*>(a.x + ((long long)sl * a.n + (t - pos)) * D + ch);
   }
+  float* sp = a.scales + slice * a.c.blocks() + blk;
+  const float was = live && b0 < pos ? *sp : 0.0f;
+  const bool has_old = was > 0.0f && was < INFINITY;  // anything else was never stored: the block is empty
+  // extremes of the lane's channels over the new tokens
+  __nv_bfloat162 lo[4], hi[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) lo[j] = as_bf16x2(kBf16Inf2), hi[j] = as_bf16x2(kBf16NegInf2);
 #pragma unroll
   for (int i = 0; i < NL; ++i) {
-    m = fmaxf(m, fmaxf(fabsf(bf16lo(x[i].x)), fabsf(bf16hi(x[i].x))));
-    m = fmaxf(m, fmaxf(fabsf(bf16lo(x[i].y)), fabsf(bf16hi(x[i].y))));
-  }
-  m = warp_max_f32(m);
-  if (lane == 0) s_max[warp] = m;
-  __syncthreads();
-  for (int i = 0; i < wpb; ++i) m = fmaxf(m, s_max[warp - part + i]);
-  int e = cache8_exponent<CODE>(m);
-  float ratio = 1.0f;
-  bool grew = false;
-  float* sp = a.scales + slice * a.c.blocks() + blk;
-  const float was = has_old ? *sp : 0.0f;
-  has_old = was > 0.0f && was < INFINITY;  // anything else was never stored: the block is empty
-  if (has_old) {
-    grew = two_to(e) > was;
-    if (grew) {
-      ratio = was * two_to(-e);
-    } else {
-      e = (int)(__float_as_uint(was) >> 23) - 127;
+    const int t = t0 + i * TPL;
+    if (live && t >= pos && t < end) {
+      const uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) lo[j] = __hmin2(lo[j], as_bf16x2(v[j])), hi[j] = __hmax2(hi[j], as_bf16x2(v[j]));
     }
   }
-  const float inv = two_to(-e);
-  float lo[4], hi[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) lo[j] = 448.0f, hi[j] = -448.0f;
+  for (int o = LPT; o < 32; o <<= 1)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      lo[j] = __hmin2(lo[j], as_bf16x2(__shfl_xor_sync(0xffffffffu, as_u32(lo[j]), o)));
+      hi[j] = __hmax2(hi[j], as_bf16x2(__shfl_xor_sync(0xffffffffu, as_u32(hi[j]), o)));
+    }
+  float m = 0.0f;  // (a lane without new tokens has -inf and inf: no maximum)
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 l2 = __bfloat1622float2(lo[j]), h2 = __bfloat1622float2(hi[j]);
+    if (l2.x <= h2.x) m = fmaxf(fmaxf(m, fmaxf(fabsf(l2.x), fabsf(h2.x))), fmaxf(fabsf(l2.y), fabsf(h2.y)));
+  }
+  m = warp_max_f32(m);
+  if (wpb > 1) {
+    if (lane == 0) s_max[warp] = m;
+    __syncthreads();
+    for (int i = 0; i < wpb; ++i) m = fmaxf(m, s_max[warp - part + i]);
+  }
+  int e = cache8_exponent<CODE>(m);
+  const bool grew = has_old && two_to(e) > was;
+  const float ratio = grew ? was * two_to(-e) : 1.0f;
+  if (has_old && !grew) e = (int)(__float_as_uint(was) >> 23) - 127;
+  const float inv = two_to(-e);
   uint8_t* row = a.codes + slice * a.c.k.T * D + ch;
 #pragma unroll
   for (int i = 0; i < NL; ++i) {
     const int t = t0 + i * TPL;
-    const bool is_new = live && t >= pos && t < end;
-    if (is_new || (grew && t < pos)) {
-      float v[4];
-      uint32_t* at = reinterpret_cast<uint32_t*>(row + (long long)t * D);
-      if (is_new) {
-        v[0] = bf16lo(x[i].x) * inv, v[1] = bf16hi(x[i].x) * inv, v[2] = bf16lo(x[i].y) * inv, v[3] = bf16hi(x[i].y) * inv;
-      } else {
-        unpack_codes<CODE>(*at, v);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] *= ratio;
-      }
-      const uint32_t c = pack_codes<CODE>(v);
-      *at = c;
-      unpack_codes<CODE>(c, v);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) lo[j] = fminf(lo[j], v[j]), hi[j] = fmaxf(hi[j], v[j]);
+    if (live && t >= pos && t < end) {
+      uint2 c;
+      c.x = pack_codes<CODE>(bf16lo(x[i].x) * inv, bf16hi(x[i].x) * inv, bf16lo(x[i].y) * inv, bf16hi(x[i].y) * inv);
+      c.y = pack_codes<CODE>(bf16lo(x[i].z) * inv, bf16hi(x[i].z) * inv, bf16lo(x[i].w) * inv, bf16hi(x[i].w) * inv);
+      *reinterpret_cast<uint2*>(row + (long long)t * D) = c;
     }
   }
   const bool keys = a.bounds != nullptr && s == 0;
-  // the block's warps share their extremes; every warp of the CTA comes this way
-  if constexpr (TPL == 2) {
+  // code values of the extremes, by the same rounding
+  float vlo[8], vhi[8];
+  if (keys || grew) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      lo[j] = fminf(lo[j], __shfl_xor_sync(0xffffffffu, lo[j], 16));
-      hi[j] = fmaxf(hi[j], __shfl_xor_sync(0xffffffffu, hi[j], 16));
+    for (int j = 0; j < 4; j += 2) {
+      const float2 l0 = __bfloat1622float2(lo[j]), l1 = __bfloat1622float2(lo[j + 1]);
+      const float2 h0 = __bfloat1622float2(hi[j]), h1 = __bfloat1622float2(hi[j + 1]);
+      float v[4];
+      unpack_codes<CODE>(pack_codes<CODE>(l0.x * inv, l0.y * inv, l1.x * inv, l1.y * inv), v);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) vlo[2 * j + k] = l0.x <= h0.x ? v[k] : 448.0f;
+      unpack_codes<CODE>(pack_codes<CODE>(h0.x * inv, h0.y * inv, h1.x * inv, h1.y * inv), v);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) vhi[2 * j + k] = l0.x <= h0.x ? v[k] : -448.0f;
     }
   }
-  if (sub == 0) {
+  if (grew) {  // the block's older codes, rounded anew
+    for (int t = t0; t < min(pos, (int)b0 + 16 * part + 16); t += TPL) {
+      uint2* at = reinterpret_cast<uint2*>(row + (long long)t * D);
+      uint2 c = *at;
+      float v[8];
+      unpack_codes<CODE>(c.x, *reinterpret_cast<float(*)[4]>(v));
+      unpack_codes<CODE>(c.y, *reinterpret_cast<float(*)[4]>(v + 4));
+      c.x = pack_codes<CODE>(v[0] * ratio, v[1] * ratio, v[2] * ratio, v[3] * ratio);
+      c.y = pack_codes<CODE>(v[4] * ratio, v[5] * ratio, v[6] * ratio, v[7] * ratio);
+      *at = c;
+      unpack_codes<CODE>(c.x, *reinterpret_cast<float(*)[4]>(v));
+      unpack_codes<CODE>(c.y, *reinterpret_cast<float(*)[4]>(v + 4));
 #pragma unroll
-    for (int j = 0; j < 4; ++j) s_lo[warp][ch + j] = lo[j], s_hi[warp][ch + j] = hi[j];
+      for (int j = 0; j < 8; ++j) vlo[j] = fminf(vlo[j], v[j]), vhi[j] = fmaxf(vhi[j], v[j]);
+    }
   }
-  __syncthreads();  // also: every warp of the block has read the old scale
-  if (live && part == 0 && sub == 0) {
-    if (lane == 0) *sp = two_to(e);
+  if (__syncthreads_or(keys && (wpb > 1 || grew))) {  // extremes that lie in several lanes or warps
     if (keys) {
+#pragma unroll
+      for (int o = LPT; o < 32; o <<= 1)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          vlo[j] = fminf(vlo[j], __shfl_xor_sync(0xffffffffu, vlo[j], o));
+          vhi[j] = fmaxf(vhi[j], __shfl_xor_sync(0xffffffffu, vhi[j], o));
+        }
+      if (sub == 0) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s_lo[warp][ch + j] = vlo[j], s_hi[warp][ch + j] = vhi[j];
+      }
+    }
+    __syncthreads();
+    if (keys && part == 0) {
       for (int i = 1; i < wpb; ++i) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) lo[j] = fminf(lo[j], s_lo[warp + i][ch + j]), hi[j] = fmaxf(hi[j], s_hi[warp + i][ch + j]);
+        for (int j = 0; j < 8; ++j) vlo[j] = fminf(vlo[j], s_lo[warp + i][ch + j]), vhi[j] = fmaxf(vhi[j], s_hi[warp + i][ch + j]);
       }
+    }
+  }
+  // (every warp of the block has read the old scale before the barrier above)
+  if (live && part == 0) {
+    if (lane == 0) *sp = two_to(e);
+    if (keys && sub == 0) {
       const long long unit = ((long long)(a.l0 + lz) * a.c.k.B + b) * a.c.k.H + h;
-      char4* at = reinterpret_cast<char4*>(a.bounds + (unit * a.c.blocks() + blk) * 2 * D + ch);
-      int l4[4], h4[4];
+      uint2* at = reinterpret_cast<uint2*>(a.bounds + (unit * a.c.blocks() + blk) * 2 * D + ch);
+      int l8[8], h8[8];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) l4[j] = low_bound<CODE>(lo[j]), h4[j] = high_bound<CODE>(hi[j]);
+      for (int j = 0; j < 8; ++j) l8[j] = low_bound<CODE>(vlo[j]), h8[j] = high_bound<CODE>(vhi[j]);
       if (has_old && !grew) {
-        const char4 pl = at[0], ph = at[D / 4];
-        l4[0] = min(l4[0], (int)pl.x), l4[1] = min(l4[1], (int)pl.y), l4[2] = min(l4[2], (int)pl.z), l4[3] = min(l4[3], (int)pl.w);
-        h4[0] = max(h4[0], (int)ph.x), h4[1] = max(h4[1], (int)ph.y), h4[2] = max(h4[2], (int)ph.z), h4[3] = max(h4[3], (int)ph.w);
+        const uint2 pl = at[0], ph = at[D / 8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          l8[j] = min(l8[j], (int)(int8_t)((j < 4 ? pl.x : pl.y) >> (8 * (j & 3))));
+          h8[j] = max(h8[j], (int)(int8_t)((j < 4 ? ph.x : ph.y) >> (8 * (j & 3))));
+        }
       }
-      at[0] = make_char4(l4[0], l4[1], l4[2], l4[3]);
-      at[D / 4] = make_char4(h4[0], h4[1], h4[2], h4[3]);
+      uint32_t l[2] = {0, 0}, hh[2] = {0, 0};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        l[j >> 2] |= ((uint32_t)l8[j] & 255u) << (8 * (j & 3));
+        hh[j >> 2] |= ((uint32_t)h8[j] & 255u) << (8 * (j & 3));
+      }
+      at[0] = make_uint2(l[0], l[1]);
+      at[D / 8] = make_uint2(hh[0], hh[1]);
     }
   }
 }
@@ -200,16 +246,15 @@ long long append_ctas(const Cache8AppendArgs& a) {
 
 }  // namespace
 
-bool cache8_append_fits(const Cache8AppendArgs& a) { return append_ctas(a) < (1LL << 31); }
+bool cache8_append_fits(const Cache8AppendArgs& a) {
+  return append_ctas(a) * (kWarps / (a.c.tb / 16)) < (1LL << 31);
+}
 
 cudaError_t launch_cache8_append(const Cache8AppendArgs& a, cudaStream_t st) {
-  const unsigned grid = (unsigned)append_ctas(a);
   const bool i8 = a.c.code == kCache8Int8;
-  if (a.c.k.d == 128)
-    i8 ? append_kernel<128, kCache8Int8><<<grid, kWarps * 32, 0, st>>>(a) : append_kernel<128, kCache8E4m3><<<grid, kWarps * 32, 0, st>>>(a);
-  else
-    i8 ? append_kernel<64, kCache8Int8><<<grid, kWarps * 32, 0, st>>>(a) : append_kernel<64, kCache8E4m3><<<grid, kWarps * 32, 0, st>>>(a);
-  return cudaGetLastError();
+  auto kern = a.c.k.d == 128 ? (i8 ? append_kernel<128, kCache8Int8> : append_kernel<128, kCache8E4m3>)
+                             : (i8 ? append_kernel<64, kCache8Int8> : append_kernel<64, kCache8E4m3>);
+  return launch_after(kern, dim3((unsigned)append_ctas(a)), kWarps * 32, 0, st, 1, a);
 }
 
 }  // namespace cg

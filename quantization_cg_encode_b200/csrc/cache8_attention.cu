@@ -135,8 +135,8 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 && NT == 2 ? 1 : 2) cach
   uint32_t matrix_piece[CH / 2];
 #pragma unroll
   for (int jj = 0; jj < CH / 2; ++jj) matrix_piece[jj] = piece_at<D>(lane & 15, 2 * jj + (lane >> 4));
-  dependents_may_launch();
   previous_kernel_done();
+  dependents_may_launch();
 
   int lz = 0, b = 0, idx = 0, tile0 = 0, tiles = 0;
   int unit_at = 0;  // the unit's first tile in the row of all tiles
@@ -535,8 +535,8 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 && NT == 2 ? 1 : 2) cach
 template <int D>
 __global__ void __launch_bounds__(D) cache8_combine_kernel(Cache8AttnArgs a, bool mass) {
   const int R = 8 * a.nt, ch = threadIdx.x, r = blockIdx.y;
-  dependents_may_launch();
   previous_kernel_done();
+  dependents_may_launch();
   const Tail tail = reinterpret_cast<const Tail*>(a.tails)[blockIdx.x];
   if (r >= tail.rows || tail.pieces == 0) return;
   auto piece = [&](int i) {  // 0: the last
@@ -562,8 +562,8 @@ __global__ void __launch_bounds__(256) cache8_mass_kernel(Cache8AttnArgs a, int 
   __shared__ float s_sum[8][32];
   const int H = a.c.k.H, B = a.c.k.B, nb = a.c.blocks();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  dependents_may_launch();
   previous_kernel_done();
+  dependents_may_launch();
   const long long u = blockIdx.x / chunks;
   const int blk = (blockIdx.x % chunks) * 32 + lane;
   const int h = (int)(u % H), b = (int)((u / H) % B), lz = (int)(u / H / B);
