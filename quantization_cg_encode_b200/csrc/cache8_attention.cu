@@ -37,11 +37,14 @@ namespace cg {
 namespace {
 
 constexpr int kWarps = 8;
+// CTAs an SM: 16 query rows at d = 128 leave registers for one.  (With their q in shared memory 12
+// and 16 warps fit; four draft tokens with block weights took 74 us with 8, 88 with 12, 96 with 16.)
+constexpr int ctas_per_sm(int d, int nt) { return d == 128 && nt == 2 ? 1 : 2; }
 constexpr int kStages = 3;
 constexpr int kSms = 148;               // what the number of CTAs is sized for
-constexpr int kLeastRun = kWarps;       // tiles: one a warp
+constexpr int kLeastRun = 8;            // tiles of a run at least
 constexpr int kMaxCluster = 8;
-constexpr int kClusterTiles = 6;        // tiles that a warp takes in about the time of a second kernel
+constexpr int kClusterTiles = 16;       // tiles of a warp in a unit that a cluster takes
 constexpr float kNone = -1.0e30f;       // a running maximum that has seen nothing
 constexpr float kLag = 8.0f;            // how far a value may lie above the running maximum
 constexpr float kShift = 7.0f;          // 2^kShift p' <= 2^15 fits fp16
@@ -113,7 +116,7 @@ struct Tail {
 }  // namespace
 
 template <int D, int CODE, int NT, bool SPARSE, bool MASS>
-__global__ void __launch_bounds__(kWarps * 32, D == 128 && NT == 2 ? 1 : 2) cache8_attn_kernel(Cache8AttnArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, ctas_per_sm(D, NT)) cache8_attn_kernel(Cache8AttnArgs a) {
   constexpr int R = 8 * NT, CH = D / 16, TILE = 16 * D;  // CH: 16-byte pieces of a row
   __shared__ float s_m[kWarps][R], s_mv[kWarps][R], s_l[kWarps][R];
   __shared__ float s_w[kWarps][R], s_fin[R][3];
@@ -296,7 +299,7 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 && NT == 2 ? 1 : 2) cach
     }
 
     float o[NT][CH][4];
-    float m_run[NT][2], mv_run[NT][2], l_run[NT][2];
+    float m_run[NT][2], mv_run[NT][2], mv_m[NT][2], l_run[NT][2];  // mv_m: M' - M
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -304,7 +307,7 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 && NT == 2 ? 1 : 2) cach
 #pragma unroll
         for (int j = 0; j < 4; ++j) o[nt][i][j] = 0.0f;
 #pragma unroll
-      for (int j = 0; j < 2; ++j) m_run[nt][j] = mv_run[nt][j] = kNone, l_run[nt][j] = 0.0f;
+      for (int j = 0; j < 2; ++j) m_run[nt][j] = mv_run[nt][j] = kNone, mv_m[nt][j] = l_run[nt][j] = 0.0f;
     }
 
     for (int i0 = 0; i0 < n_mine; i0 += kStages) {
@@ -342,31 +345,36 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 && NT == 2 ? 1 : 2) cach
           for (int nt = 0; nt < NT; ++nt) mma_f16_16816(s[nt], af, bq[nt][2 * jj + k][0], bq[nt][2 * jj + k][1]);
         }
       }
-      // s[nt][0..3]: token g (0, 1) or g + 8 (2, 3), row 2c + (index & 1)
+      // s[nt][0..3]: token g (0, 1) or g + 8 (2, 3), row 2c + (index & 1); x = factor s
+      float factor[NT][2], x[NT][4];  // x - M
       bool over = false;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const float f = kscale * qs[nt][j];
-          s[nt][j] *= f, s[nt][j + 2] *= f;
+          factor[nt][j] = fmaxf(kscale * qs[nt][j], 1.0e-37f);  // (0 times -inf is no -inf)
           if (t0 + 16 > all_see) {
             const int t = t0 + g, see = min(lim[nt][j], end);
             s[nt][j] = t < see ? s[nt][j] : -INFINITY;
             s[nt][j + 2] = t + 8 < see ? s[nt][j + 2] : -INFINITY;
           }
-          over |= fmaxf(s[nt][j], s[nt][j + 2]) > fminf(m_run[nt][j], mv_run[nt][j] - vexp) + kLag;
+          x[nt][j] = __fmaf_rn(s[nt][j], factor[nt][j], -m_run[nt][j]);
+          x[nt][j + 2] = __fmaf_rn(s[nt][j + 2], factor[nt][j], -m_run[nt][j]);
+          over |= fmaxf(x[nt][j], x[nt][j + 2]) > fminf(kLag, mv_m[nt][j] + (kLag - vexp));
         }
       if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const float top = column_max(fmaxf(s[nt][j], s[nt][j + 2]));
-            const float m = fmaxf(m_run[nt][j], top), mv = fmaxf(mv_run[nt][j], top + vexp);
-            const float f = ex2(m_run[nt][j] - m), fv = ex2(mv_run[nt][j] - mv);
-            m_run[nt][j] = m, mv_run[nt][j] = mv;
-            l_run[nt][j] *= f;
+            const float top = column_max(fmaxf(s[nt][j], s[nt][j + 2])) * factor[nt][j];
+            const float m_old = m_run[nt][j], mv_old = mv_run[nt][j];
+            const float m = fmaxf(m_old, top), mv = fmaxf(mv_old, top + vexp);
+            const float fv = ex2(mv_old - mv);
+            m_run[nt][j] = m, mv_run[nt][j] = mv, mv_m[nt][j] = mv - m;
+            l_run[nt][j] *= ex2(m_old - m);
+            x[nt][j] = __fmaf_rn(s[nt][j], factor[nt][j], -m);
+            x[nt][j + 2] = __fmaf_rn(s[nt][j + 2], factor[nt][j], -m);
 #pragma unroll
             for (int k = 0; k < CH; ++k) o[nt][k][j] *= fv, o[nt][k][j + 2] *= fv;
           }
@@ -377,12 +385,12 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 && NT == 2 ? 1 : 2) cach
         float pv[4], tile_sum[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const float p0 = ex2(s[nt][j] - m_run[nt][j]), p1 = ex2(s[nt][j + 2] - m_run[nt][j]);
+          const float p0 = ex2(x[nt][j]), p1 = ex2(x[nt][j + 2]);
           tile_sum[j] = p0 + p1;
           l_run[nt][j] += tile_sum[j];
           // p s_V relative to M': p 2^f <= 2^(kLag + kShift), so a factor of over 2^100 meets a p below 2^-85, whose
           // row's sum holds a weight of 1 at least: nothing that a result in fp32 could show
-          const float f = ex2(fminf(m_run[nt][j] - mv_run[nt][j] + (vexp + kShift), 100.0f));
+          const float f = ex2(fminf((vexp + kShift) - mv_m[nt][j], 100.0f));
           pv[j] = p0 * f, pv[j + 2] = p1 * f;
         }
 #pragma unroll
@@ -611,15 +619,19 @@ void plan(Cache8AttnArgs& a) {
   const int rows = a.n_select ? a.gq : a.gq * a.nq;
   a.nt = rows > 8 ? 2 : 1;
   a.row_tiles = (rows + 8 * a.nt - 1) / (8 * a.nt);
-  const long long most = kSms * (a.nt == 2 && a.c.k.d == 128 ? 1 : 2);
+  const long long most = kSms * ctas_per_sm(a.c.k.d, a.nt);
   const long long runs = (tiles_of(a) + kLeastRun - 1) / kLeastRun;
   a.ctas = (int)(runs < most ? runs : most);
   // clusters: as many CTAs as give each warp one tile of the longest unit, where the GPU holds them
-  // all at once and no warp gets more than kClusterTiles
+  // all at once.  A unit that is shorter than the others leaves its CTAs idle, so no warp may get
+  // more than kClusterTiles, unless all units are of one length (one sequence) and fill the GPU:
+  // there 32 layers of 1024 (2048, 4096) tokens took 18.2 (27.9, 48.1) us, with equal runs and the
+  // second kernel 24.3 (33.5, 50.9).
   const long long unit = a.n_select ? (long long)a.n_select * (a.c.tb / 16) : (a.max_tokens + 15) / 16;
   int size = 1;
   while (size < kMaxCluster && size * kWarps < unit && units(a) * size * 2 <= most) size *= 2;
-  a.cluster = units(a) <= most && unit <= (long long)size * kWarps * kClusterTiles ? size : 0;
+  const bool even = a.c.k.B == 1 && a.nq == 1 && 4 * units(a) * size >= 3 * most;
+  a.cluster = units(a) <= most && (even || unit <= (long long)size * kWarps * kClusterTiles) ? size : 0;
   if (a.cluster) a.ctas = (int)units(a) * size;
 }
 
