@@ -68,40 +68,54 @@ __device__ __forceinline__ uint32_t as_u32(__nv_bfloat162 v) { return *reinterpr
 constexpr uint32_t kBf16Inf2 = 0x7F807F80u, kBf16NegInf2 = 0xFF80FF80u;
 
 template <int D, int CODE>
-__global__ void __launch_bounds__(kWarps * 32) append_kernel(Cache8AppendArgs a) {
+__global__ void __launch_bounds__(kWarps * 32) append_kernel(Cache8AppendArgs a, unsigned window, int tb_shift) {
   constexpr int LPT = D / 8;         // lanes a token
   constexpr int TPL = 32 / LPT;      // tokens a warp loads at once: 2 or 4
   constexpr int NL = 16 / TPL;       // loads of a warp
   __shared__ float s_max[kWarps];
   __shared__ float s_lo[kWarps][D], s_hi[kWarps][D];  // extremes of the code values
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int tb = a.c.tb, wpb = tb >> 4;               // warps of a block: 1, 2 or 4
-  const int window = (a.n + tb - 2) / tb + 1;         // blocks that n tokens touch at most
-  const int items = a.nl * 2 * a.c.k.B * a.c.k.H * window;
-  const int item = blockIdx.x * (kWarps / wpb) + warp / wpb;  // (slice, block of the window)
-  const int part = warp % wpb;
-  const bool inside = item < items;
-  const int sl = inside ? item / window : 0, w = inside ? item % window : 0;
-  const int h = sl % a.c.k.H, b = sl / a.c.k.H % a.c.k.B, s = sl / a.c.k.H / a.c.k.B & 1, lz = sl / a.c.k.H / a.c.k.B >> 1;
+  const int wpb = 1 << (tb_shift - 4);                // warps of a block: 1, 2 or 4
+  // (slice, block of the window: the blocks that n tokens touch at most)
+  const unsigned item = blockIdx.x * (kWarps >> (tb_shift - 4)) + (warp >> (tb_shift - 4));
+  const int part = warp & (wpb - 1);
+  const unsigned H = a.c.k.H, B = a.c.k.B, slices = a.nl * 2 * B * H;
+  unsigned sl = item / window;
+  const bool inside = sl < slices;
+  if (!inside) sl = 0;
+  const int w = inside ? (int)(item - sl * window) : 0;
+  const unsigned bh = sl / H, ls = bh / B;
+  const int h = (int)(sl - bh * H), b = (int)(bh - ls * B), s = (int)(ls & 1u), lz = (int)(ls >> 1);
   previous_kernel_done();
   const int pos = a.pos[b];
   const int cnt = min(a.n, a.counts ? a.counts[b] : a.n);
   // tokens [pos, end) are new; positions off the cache are not written
   const int end = pos < 0 || cnt <= 0 ? 0 : (int)min((long long)pos + cnt, (long long)a.c.k.T);
-  const long long b0 = pos < 0 ? 0 : ((long long)(pos / tb) + w) * tb;  // the block's first token
+  const long long b0 = pos < 0 ? 0 : ((long long)(pos >> tb_shift) + w) << tb_shift;  // the block's first token
   const bool live = inside && pos >= 0 && b0 < end;
   if (__syncthreads_or(live) == 0) return;
-  const int blk = live ? (int)(b0 / tb) : 0;
+  const int blk = live ? (int)(b0 >> tb_shift) : 0;
   const long long slice = (((long long)(a.l0 + lz) * 2 + s) * a.c.k.B + b) * a.c.k.H + h;
 
   const int ch = 8 * (lane % LPT), sub = lane / LPT;  // channels [ch, ch + 8), token of the load
   const int t0 = (live ? (int)b0 : 0) + 16 * part + sub;
+  // tokens t0, t0 + TPL, ... of the lane; `all`: the warp's 16 tokens are new
+  const int first = (live ? (int)b0 : 0) + 16 * part;
+  const bool all = live && first >= pos && first + 16 <= end;
+  const uint4* from = reinterpret_cast<const uint4*>(a.x + ((long long)sl * a.n + (t0 - pos)) * D + ch);
   uint4 x[NL];
+  unsigned fresh = 0;  // bit i: the lane's token i is new
+  if (all) {
 #pragma unroll
-  for (int i = 0; i < NL; ++i) {
-    const int t = t0 + i * TPL;
-    x[i] = make_uint4(0, 0, 0, 0);
-    if (live && t >= pos && t < end) x[i] = *reinterpret_cast<const uint4*>(a.x + ((long long)sl * a.n + (t - pos)) * D + ch);
+    for (int i = 0; i < NL; ++i) x[i] = from[i * 32];  // 32 lanes of 16 bytes: TPL tokens
+    fresh = (1u << NL) - 1;
+  } else {
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+      const int t = t0 + i * TPL;
+      x[i] = make_uint4(0, 0, 0, 0);
+      if (live && t >= pos && t < end) x[i] = from[i * 32], fresh |= 1u << i;
+    }
   }
   float* sp = a.scales + slice * a.c.blocks() + blk;
   const float was = live && b0 < pos ? *sp : 0.0f;
@@ -110,14 +124,18 @@ __global__ void __launch_bounds__(kWarps * 32) append_kernel(Cache8AppendArgs a)
   __nv_bfloat162 lo[4], hi[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) lo[j] = as_bf16x2(kBf16Inf2), hi[j] = as_bf16x2(kBf16NegInf2);
+  auto widen = [&](const uint4& y) {
+    const uint32_t v[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-  for (int i = 0; i < NL; ++i) {
-    const int t = t0 + i * TPL;
-    if (live && t >= pos && t < end) {
-      const uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+    for (int j = 0; j < 4; ++j) lo[j] = __hmin2(lo[j], as_bf16x2(v[j])), hi[j] = __hmax2(hi[j], as_bf16x2(v[j]));
+  };
+  if (all) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) lo[j] = __hmin2(lo[j], as_bf16x2(v[j])), hi[j] = __hmax2(hi[j], as_bf16x2(v[j]));
-    }
+    for (int i = 0; i < NL; ++i) widen(x[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < NL; ++i)
+      if (fresh >> i & 1u) widen(x[i]);
   }
 #pragma unroll
   for (int o = LPT; o < 32; o <<= 1)
@@ -144,15 +162,20 @@ __global__ void __launch_bounds__(kWarps * 32) append_kernel(Cache8AppendArgs a)
   if (has_old && !grew) e = (int)(__float_as_uint(was) >> 23) - 127;
   const float inv = two_to(-e);
   uint8_t* row = a.codes + slice * a.c.k.T * D + ch;
+  uint2* to = reinterpret_cast<uint2*>(row + (long long)t0 * D);
+  auto coded = [&](const uint4& y) {
+    uint2 c;
+    c.x = pack_codes<CODE>(bf16lo(y.x) * inv, bf16hi(y.x) * inv, bf16lo(y.y) * inv, bf16hi(y.y) * inv);
+    c.y = pack_codes<CODE>(bf16lo(y.z) * inv, bf16hi(y.z) * inv, bf16lo(y.w) * inv, bf16hi(y.w) * inv);
+    return c;
+  };
+  if (all) {
 #pragma unroll
-  for (int i = 0; i < NL; ++i) {
-    const int t = t0 + i * TPL;
-    if (live && t >= pos && t < end) {
-      uint2 c;
-      c.x = pack_codes<CODE>(bf16lo(x[i].x) * inv, bf16hi(x[i].x) * inv, bf16lo(x[i].y) * inv, bf16hi(x[i].y) * inv);
-      c.y = pack_codes<CODE>(bf16lo(x[i].z) * inv, bf16hi(x[i].z) * inv, bf16lo(x[i].w) * inv, bf16hi(x[i].w) * inv);
-      *reinterpret_cast<uint2*>(row + (long long)t * D) = c;
-    }
+    for (int i = 0; i < NL; ++i) to[i * 32] = coded(x[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < NL; ++i)
+      if (fresh >> i & 1u) to[i * 32] = coded(x[i]);
   }
   const bool keys = a.bounds != nullptr && s == 0;
   // code values of the extremes, by the same rounding
@@ -172,7 +195,7 @@ __global__ void __launch_bounds__(kWarps * 32) append_kernel(Cache8AppendArgs a)
     }
   }
   if (grew) {  // the block's older codes, rounded anew
-    for (int t = t0; t < min(pos, (int)b0 + 16 * part + 16); t += TPL) {
+    for (int t = t0; t < min(pos, first + 16); t += TPL) {
       uint2* at = reinterpret_cast<uint2*>(row + (long long)t * D);
       uint2 c = *at;
       float v[8];
@@ -238,9 +261,10 @@ __global__ void __launch_bounds__(kWarps * 32) append_kernel(Cache8AppendArgs a)
   }
 }
 
+long long append_window(const Cache8AppendArgs& a) { return (a.n + a.c.tb - 2) / a.c.tb + 1; }
 long long append_ctas(const Cache8AppendArgs& a) {
-  const int per = kWarps / (a.c.tb / 16), window = (a.n + a.c.tb - 2) / a.c.tb + 1;
-  const long long items = (long long)a.nl * 2 * a.c.k.B * a.c.k.H * window;
+  const int per = kWarps / (a.c.tb / 16);
+  const long long items = (long long)a.nl * 2 * a.c.k.B * a.c.k.H * append_window(a);
   return (items + per - 1) / per;
 }
 
@@ -254,7 +278,8 @@ cudaError_t launch_cache8_append(const Cache8AppendArgs& a, cudaStream_t st) {
   const bool i8 = a.c.code == kCache8Int8;
   auto kern = a.c.k.d == 128 ? (i8 ? append_kernel<128, kCache8Int8> : append_kernel<128, kCache8E4m3>)
                              : (i8 ? append_kernel<64, kCache8Int8> : append_kernel<64, kCache8E4m3>);
-  return launch_after(kern, dim3((unsigned)append_ctas(a)), kWarps * 32, 0, st, 1, a);
+  const int tb_shift = a.c.tb == 16 ? 4 : a.c.tb == 32 ? 5 : 6;
+  return launch_after(kern, dim3((unsigned)append_ctas(a)), kWarps * 32, 0, st, 1, a, (unsigned)append_window(a), tb_shift);
 }
 
 }  // namespace cg
