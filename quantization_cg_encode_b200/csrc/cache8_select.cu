@@ -8,16 +8,26 @@
 // block's score for a query token is its largest over the query heads of the KV head.  The sums
 // are whole numbers below 2^21 and the factors powers of two: every step is exact in fp32, so the
 // choice does not depend on the order of the sums, and ties go to the lowest index.
+//
+// The scores are a product of the bounds (16 blocks a warp) with the rows (8 at a time) on the
+// integer tensor path, mma.sync m16n8k32: the bytes go from memory to operands as they are.  A
+// cluster scores the blocks of one KV head, and one of its CTAs chooses among them for each query
+// token from the shared memory of all: one kernel, whose time is its latency where few blocks are
+// scored and the reading of the bounds where many are.  Beyond kPickKeys blocks the scores go
+// through the workspace to a second kernel.
+#include <cooperative_groups.h>
+
 #include "cache8.cuh"
 
 namespace cg {
 
 namespace {
 
-constexpr int kScoreThreads = 256;
-constexpr int kScoreBlocks = kScoreThreads / 4;  // blocks of the cache that a CTA scores at a time
-constexpr int kPickThreads = 512;
-constexpr int kPickKeys = 8192;                  // keys that the choosing CTA holds in shared memory
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kStep = kWarps * 16;     // blocks that a CTA scores at a time
+constexpr int kPickRegs = 8 * kThreads;  // keys that a choosing CTA holds in registers
+constexpr int kPickKeys = 8192;          // and in the shared memory of its cluster
+constexpr int kListed = 8192;            // blocks that an evicting CTA lists in shared memory
 constexpr int kSms = 148;
 
 // fp32 as an unsigned key of the same order; -0 is 0, NaN comes below everything
@@ -30,216 +40,319 @@ __device__ __forceinline__ uint32_t order_key(float f) {
 // Blocks [0, nb) a query token sees
 __device__ __forceinline__ int seen_blocks(int n, int nq, int i, int tb) { return (max(0, n - nq + 1 + i) + tb - 1) / tb; }
 
-}  // namespace
-
-// scores[unit][i][block]: four lanes share a block (d / 4 channels each, both bounds), eight blocks a
-// warp; the bounds stay in registers for all rows of the unit, and those of the CTA's next blocks
-// are on their way meanwhile.
-template <int D>
-__global__ void __launch_bounds__(kScoreThreads) cache8_score_kernel(Cache8SelectArgs a, int chunks, int per, int nb_max) {
-  constexpr int Q = D / 64;               // 16-byte words of a lane's channels
-  extern __shared__ uint4 sq[];           // [rows][2][D / 16]: q8 >= 0, q8 <= 0
-  const int rows = a.gq * a.nq;
-  float* unit = reinterpret_cast<float*>(sq + rows * (D / 8));  // [rows] 2^e
-  const int H = a.c.k.H, B = a.c.k.B;
-  const int u = blockIdx.x / chunks, chunk = blockIdx.x % chunks;
-  const int h = u % H, b = u / H % B, lz = u / H / B;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = lane & 3;
-  const long long slice = ((long long)(a.l0 + lz) * B + b) * H + h;
-  const uint4* bounds = reinterpret_cast<const uint4*>(a.bounds + slice * a.c.blocks() * 2 * D) + part;
-  const float* scales = a.scales + (((long long)(a.l0 + lz) * 2 * B + b) * H + h) * a.c.blocks();
-  previous_kernel_done();
-  const int n = max(0, min(a.lens[b], a.max_tokens));
-  const int nb = (n + a.c.tb - 1) / a.c.tb;
-  const int end = min(nb, (chunk + 1) * per);
-  int blk = chunk * per + warp * 8 + (lane >> 2);
-  if (chunk * per >= nb) return;
-  uint4 lo[Q], hi[Q];
-  float sk = 0.0f;
-  auto load = [&](int at) {
-#pragma unroll
-    for (int j = 0; j < Q; ++j) lo[j] = hi[j] = make_uint4(0, 0, 0, 0);
-    if (at < end) {
-#pragma unroll
-      for (int j = 0; j < Q; ++j) lo[j] = bounds[(long long)at * (D / 8) + 4 * j], hi[j] = bounds[(long long)at * (D / 8) + D / 16 + 4 * j];
-      sk = scales[at];
-    }
-  };
-  load(blk);
-  for (int r = warp; r < rows; r += kScoreThreads / 32) {
-    const uint16_t* q = a.q + ((long long)u * rows + r) * D;
-    uint2 x = make_uint2(0, 0);
-    if (lane < D / 4) x = *reinterpret_cast<const uint2*>(q + 4 * lane);
-    const float v[4] = {bf16lo(x.x), bf16hi(x.x), bf16lo(x.y), bf16hi(x.y)};
-    const float m = warp_max_f32(fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3]))));
-    const int e = cache8_exponent<kCache8Int8>(m);
-    const float inv = two_to(-e);
-    uint32_t up = 0, dn = 0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int i = max(-127, min(127, __float2int_rn(v[j] * inv)));
-      up |= ((uint32_t)max(i, 0) & 255u) << (8 * j);
-      dn |= ((uint32_t)min(i, 0) & 255u) << (8 * j);
-    }
-    uint32_t* w = reinterpret_cast<uint32_t*>(sq + r * (D / 8));
-    if (lane < D / 4) w[lane] = up, w[D / 4 + lane] = dn;
-    if (lane == 0) unit[r] = two_to(e);
-  }
-  __syncthreads();
-  auto dot4 = [](const uint4& x, const uint4& y, int acc) {
-    acc = __dp4a((int)x.x, (int)y.x, acc);
-    acc = __dp4a((int)x.y, (int)y.y, acc);
-    acc = __dp4a((int)x.z, (int)y.z, acc);
-    return __dp4a((int)x.w, (int)y.w, acc);
-  };
-  float* out = a.scores + (long long)u * a.nq * nb_max;
-  for (; blk - (lane >> 2) < end; blk += kScoreBlocks) {  // warp-uniform
-    uint4 l[Q], g[Q];
-#pragma unroll
-    for (int j = 0; j < Q; ++j) l[j] = lo[j], g[j] = hi[j];
-    const float scale = sk;
-    load(blk + kScoreBlocks);
-    for (int i = 0; i < a.nq; ++i) {
-      float best = -INFINITY;
-      for (int r = i; r < rows; r += a.nq) {
-        const uint4* q = sq + r * (D / 8) + part;
-        int dot = 0;
-#pragma unroll
-        for (int j = 0; j < Q; ++j) dot = dot4(g[j], q[4 * j], dot4(l[j], q[D / 16 + 4 * j], dot));
-        dot += __shfl_xor_sync(0xffffffffu, dot, 1);
-        dot += __shfl_xor_sync(0xffffffffu, dot, 2);
-        best = fmaxf(best, (float)dot * unit[r]);
-      }
-      if (part == 0 && blk < end) out[(long long)i * nb_max + blk] = best * scale;
-    }
-  }
+__device__ __forceinline__ void imma(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-namespace {
+constexpr int kFew = 32;  // keys among which a warp finds the threshold by counting
 
 struct PickShared {
-  uint32_t key[kPickKeys];
-  uint32_t hist[2][256];
-  uint32_t warp_sum[kPickThreads / 32];
-  uint32_t least, most, found, need, whole;
+  uint4 hist[4][64];  // 256 bins a pass
+  uint32_t few[kFew];
+  uint32_t warp_sum[2][kWarps];
+  uint32_t least, most, n_few;
 };
+// Before pick_blocks, with a barrier between
+__device__ __forceinline__ void pick_prepare(PickShared& sh) {
+  sh.hist[threadIdx.x >> 6][threadIdx.x & 63] = make_uint4(0, 0, 0, 0);
+  if (threadIdx.x == 0) sh.least = 0xffffffffu, sh.most = 0, sh.n_few = 0;
+}
+static_assert(kThreads == 256, "four histograms of 64 words of 16 bytes");
 
 // The k chosen of nb blocks (nb > k), ascending, into `out`: the first `sink`, the last
 // `recent`, and of the others those of the highest keys, ties to the lowest index.  Whole CTA.
 // Radix selection finds the key of the last one taken, eight bits a pass from the first bit in
-// which the keys differ, until a pass ends with a whole bin; then one ordered pass writes the list.
-// Keys wait in shared memory, or stay where they are if there are more than kPickKeys.
-__device__ void pick_blocks(const float* key, int nb, int k, int sink, int recent, int* out, PickShared& sh) {
+// which the keys differ, until few keys are left, which are counted against one another; then one
+// ordered pass writes the list.  Every warp reads the histogram for itself: one barrier a pass.
+// A thread has KPT consecutive keys in registers, at(i) gives key i (KPT 0: a run of them, read
+// each time).
+template <int KPT, typename At>
+__device__ void pick_blocks(At at, int nb, int k, int sink, int recent, int* out, PickShared& sh) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int lo = sink, hi = nb - recent;
-  const bool held = nb <= kPickKeys;
-  auto key_at = [&](int i) { return held ? sh.key[i] : order_key(key[i]); };
-  if (tid == 0) sh.least = 0xffffffffu, sh.most = 0;
-  if (tid < 256) sh.hist[0][tid] = 0;
-  __syncthreads();
-  uint32_t least = 0xffffffffu, most = 0;
-  for (int i = lo + tid; i < hi; i += kPickThreads) {
-    const uint32_t u = order_key(key[i]);
-    if (held) sh.key[i] = u;
-    least = min(least, u), most = max(most, u);
+  uint32_t u[KPT ? KPT : 1];
+  if constexpr (KPT > 0) {
+#pragma unroll
+    for (int j = 0; j < KPT; ++j) u[j] = tid * KPT + j < nb ? at(tid * KPT + j) : 0;
   }
+  auto each = [&](auto f) {
+    if constexpr (KPT > 0) {
+#pragma unroll
+      for (int j = 0; j < KPT; ++j) {
+        const int i = tid * KPT + j;
+        if (i >= lo && i < hi) f(u[j]);
+      }
+    } else {
+      for (int i = lo + tid; i < hi; i += kThreads) f(at(i));
+    }
+  };
+  uint32_t least = 0xffffffffu, most = 0;
+  each([&](uint32_t v) { least = min(least, v), most = max(most, v); });
   least = __reduce_min_sync(0xffffffffu, least), most = __reduce_max_sync(0xffffffffu, most);
   if (lane == 0) atomicMin(&sh.least, least), atomicMax(&sh.most, most);
   __syncthreads();
-  // keys >= thr are taken for sure, of those == thr the first `need` if it is not 0
-  uint32_t need = (uint32_t)(k - sink - recent), thr = 0xffffffffu;
-  bool exact = false;  // thr is one key's value
+  // keys > thr are taken, and of those == thr the first `need`
+  uint32_t need = (uint32_t)(k - sink - recent), thr = 0xffffffffu;  // (no key is as high)
   if (need) {
     const uint32_t differ = sh.least ^ sh.most;
-    int shift = differ ? 32 - __clz(differ) : 0;             // bits below it differ
-    thr = shift < 32 ? sh.most >> shift << shift : 0;         // the bits above it are common
+    int shift = differ ? 32 - __clz(differ) : 0;       // the bits below it differ
+    thr = shift < 32 ? sh.most >> shift << shift : 0;   // the bits above it are common
+    uint32_t inside = (uint32_t)(hi - lo);              // keys with those bits
     for (int pass = 0; shift > 0; ++pass) {
-      const int width = min(8, shift), high = shift;
+      const int high = shift;
+      if (inside <= kFew) {
+        each([&](uint32_t v) {
+          if (high == 32 || (v >> high) == (thr >> high)) sh.few[atomicAdd(&sh.n_few, 1u)] = v;
+        });
+        __syncthreads();
+        const uint32_t mine = lane < inside ? sh.few[lane] : 0u;
+        uint32_t above = 0, same = 0;
+        for (uint32_t j = 0; j < inside; ++j) {
+          const uint32_t v = sh.few[j];
+          above += v > mine, same += v == mine;
+        }
+        const unsigned got = __ballot_sync(0xffffffffu, lane < inside && above < need && above + same >= need);
+        thr = __shfl_sync(0xffffffffu, mine, __ffs(got) - 1);
+        need -= __shfl_sync(0xffffffffu, above, __ffs(got) - 1);
+        break;
+      }
+      const int width = min(8, shift);
       shift -= width;
-      uint32_t* hist = sh.hist[pass & 1];
-      for (int i = lo + tid; i < hi; i += kPickThreads) {
-        const uint32_t u = key_at(i);
-        if (high == 32 || (u >> high) == (thr >> high)) atomicAdd(&hist[(u >> shift) & ((1u << width) - 1)], 1u);
-      }
-      if (tid < 256) sh.hist[(pass + 1) & 1][tid] = 0;
+      uint32_t* hist = reinterpret_cast<uint32_t*>(sh.hist[pass]);
+      each([&](uint32_t v) {
+        if (high == 32 || (v >> high) == (thr >> high)) atomicAdd(&hist[(v >> shift) & ((1u << width) - 1)], 1u);
+      });
       __syncthreads();
-      if (warp == 0) {  // the bin in which the need-th highest lies
-        uint32_t c[8], sum = 0;
+      // the bin in which the need-th highest lies: a lane's bins are 255 - 8 lane and the seven below
+      const uint4 x = sh.hist[pass][63 - 2 * lane], y = sh.hist[pass][62 - 2 * lane];
+      const uint32_t c[8] = {x.w, x.z, x.y, x.x, y.w, y.z, y.y, y.x};
+      const uint32_t sum = c[0] + c[1] + c[2] + c[3] + c[4] + c[5] + c[6] + c[7];
+      uint32_t incl = sum;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sum += c[j] = hist[255 - (8 * lane + j)];
-        uint32_t incl = sum;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
-          if (lane >= o) incl += v;
-        }
-        uint32_t above = incl - sum;
-        if (above < need && incl >= need) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            if (above + c[j] >= need) {
-              sh.found = 255 - (8 * lane + j);
-              sh.need = need - above;
-              sh.whole = above + c[j] == need;
-              break;
-            }
-            above += c[j];
-          }
-        }
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
       }
-      __syncthreads();
-      thr |= sh.found << shift;
-      need = sh.need;
-      if (sh.whole) break;
+      uint32_t above = incl - sum, bin = 255 - 8 * lane, in_bin = 0;
+      const bool mine = above < need && incl >= need;
+      bool found = false;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (!found && above + c[j] >= need) found = true, in_bin = c[j], bin -= j;
+        if (!found) above += c[j];
+      }
+      const int owner = __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
+      thr |= __shfl_sync(0xffffffffu, bin, owner) << shift;
+      need -= __shfl_sync(0xffffffffu, above, owner);
+      inside = __shfl_sync(0xffffffffu, in_bin, owner);
     }
-    // a whole bin: every key from its lower end is taken; else the bits are used up and thr is a key
-    exact = shift == 0 && !(sh.least != sh.most && sh.whole);
-    if (!exact) need = 0;
   }
-  // runs of an odd length for each thread (no two threads of a warp meet in a bank)
-  const int per = (nb + kPickThreads - 1) / kPickThreads | 1;
+  // 0: not taken, 1: taken, 2: equal to the threshold; a thread has consecutive keys
+  const int per = KPT ? KPT : (nb + kThreads - 1) / kThreads | 1;  // (odd: no two threads of a warp meet in a bank)
   const int i0 = min(nb, tid * per), i1 = min(nb, i0 + per);
-  auto kind = [&](int i) {  // 0: not taken, 1: taken, 2: equal to the threshold
-    if (i < lo || i >= hi) return 1;
-    if (thr == 0xffffffffu && !exact) return 0;
-    const uint32_t u = key_at(i);
-    return exact ? (u > thr ? 1 : u == thr ? 2 : 0) : (u >= thr ? 1 : 0);
+  auto kind = [&](int i, uint32_t v) { return i < lo || i >= hi || v > thr ? 1 : v == thr ? 2 : 0; };
+  auto ordered = [&](auto f) {
+    if constexpr (KPT > 0) {
+#pragma unroll
+      for (int j = 0; j < KPT; ++j)
+        if (tid * KPT + j < nb) f(tid * KPT + j, kind(tid * KPT + j, u[j]));
+    } else {
+      for (int i = i0; i < i1; ++i) f(i, kind(i, at(i)));
+    }
   };
   uint32_t sure = 0, equal = 0;
-  for (int i = i0; i < i1; ++i) {
-    const int t = kind(i);
-    sure += t == 1, equal += t == 2;
+  ordered([&](int, int t) { sure += t == 1, equal += t == 2; });
+  // sums over the threads before this one
+  uint32_t s_incl = sure, e_incl = equal;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t x = __shfl_up_sync(0xffffffffu, s_incl, o), y = __shfl_up_sync(0xffffffffu, e_incl, o);
+    if (lane >= o) s_incl += x, e_incl += y;
   }
-  auto before = [&](uint32_t v) {  // sum over the threads before this one
-    uint32_t incl = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t x = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += x;
-    }
-    __syncthreads();
-    if (lane == 31) sh.warp_sum[warp] = incl;
-    __syncthreads();
-    uint32_t sum = incl - v;
-#pragma unroll
-    for (int w = 0; w < kPickThreads / 32; ++w)
-      if (w < warp) sum += sh.warp_sum[w];
-    return sum;
-  };
-  uint32_t at_sure = before(sure), at_equal = exact ? before(equal) : 0;  // `exact` is uniform
-  for (int i = i0; i < i1; ++i) {
-    const int t = kind(i);
-    if (t == 1) out[at_sure++ + min(at_equal, need)] = i;
+  if (lane == 31) sh.warp_sum[0][warp] = s_incl, sh.warp_sum[1][warp] = e_incl;
+  __syncthreads();
+  sure = s_incl - sure, equal = e_incl - equal;
+  for (int w = 0; w < warp; ++w) sure += sh.warp_sum[0][w], equal += sh.warp_sum[1][w];
+  ordered([&](int i, int t) {
+    if (t == 1) out[sure++ + min(equal, need)] = i;
     if (t == 2) {
-      if (at_equal < need) out[at_sure + at_equal] = i;
-      ++at_equal;
+      if (equal < need) out[sure + equal] = i;
+      ++equal;
     }
-  }
+  });
+}
+template <typename At>
+__device__ __forceinline__ void pick_any(At at, int nb, int k, int sink, int recent, int* out, PickShared& sh) {
+  if (nb <= 2 * kThreads)
+    pick_blocks<2>(at, nb, k, sink, recent, out, sh);
+  else if (nb <= kPickRegs)
+    pick_blocks<8>(at, nb, k, sink, recent, out, sh);
+  else
+    pick_blocks<0>(at, nb, k, sink, recent, out, sh);
+}
+
+// Query rows in tiles of eight operand columns: up to eight heads make a group of 1, 2, 4 or 8
+// columns, as many query tokens to a tile as fit; more heads take two tiles a token.
+struct RowTiles {
+  int group;      // log2 of the columns of a token in a tile (a tile has 8 >> group tokens)
+  int per_token;  // log2 of the tiles of a token (0, or 1 where group is 3)
+  int count;
+};
+__host__ __device__ inline RowTiles row_tiles(int gq, int nq) {
+  RowTiles r;
+  r.group = gq <= 1 ? 0 : gq <= 2 ? 1 : gq <= 4 ? 2 : 3;
+  r.per_token = gq > 8;
+  r.count = (nq + (8 >> r.group) - 1) >> (3 - r.group) << r.per_token;
+  return r;
 }
 
 }  // namespace
 
-__global__ void __launch_bounds__(kPickThreads) cache8_pick_kernel(Cache8SelectArgs a, int nb_max) {
+// A CTA scores `per` blocks of one (layer, batch, KV head).  FUSED: the CTAs of a cluster share the
+// unit, each keeps its scores as keys, and the choice follows; else the scores go to a.scores.
+template <int D, bool FUSED>
+__global__ void __launch_bounds__(kThreads, 4) cache8_score_kernel(Cache8SelectArgs a, int chunks, int per, int nb_max) {
+  constexpr int Q = D / 64;               // 16-byte pieces of a lane, of one bound of one block
+  __shared__ PickShared sh;
+  extern __shared__ uint4 sq[];           // [tile][column][q8 <= 0, q8 >= 0][D / 16]
+  const RowTiles rt = row_tiles(a.gq, a.nq);
+  float* unit = reinterpret_cast<float*>(sq + rt.count * 8 * (D / 8));  // [tile][column] 2^e, negative: no row
+  uint32_t* keys = reinterpret_cast<uint32_t*>(unit + rt.count * 8);     // [nq][per]
+  const unsigned H = a.c.k.H, B = a.c.k.B, u = blockIdx.x / chunks, bh = u / H;
+  const int chunk = blockIdx.x % chunks, h = u - bh * H, b = bh % B, lz = bh / B;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+  const long long slice = ((long long)(a.l0 + lz) * B + b) * H + h;
+  const uint4* bounds = reinterpret_cast<const uint4*>(a.bounds + slice * a.c.blocks() * 2 * D) + c;
+  const float* scales = a.scales + (((long long)(a.l0 + lz) * 2 * B + b) * H + h) * a.c.blocks();
+  previous_kernel_done();
+  const int n = max(0, min(a.lens[b], a.max_tokens));
+  const int nb = (n + a.c.tb - 1) / a.c.tb;
+  const int begin = chunk * per, end = min(nb, begin + per);
+  if (!FUSED && begin >= nb) return;
+  uint4 x[2][2][Q];  // [block g, g + 8][low, high][piece]
+  float scale[2];
+  auto load = [&](int at) {
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int blk = at + g + 8 * r;
+#pragma unroll
+      for (int j = 0; j < Q; ++j) {
+        x[r][0][j] = blk < end ? bounds[(long long)blk * (D / 8) + 4 * j] : make_uint4(0, 0, 0, 0);
+        x[r][1][j] = blk < end ? bounds[(long long)blk * (D / 8) + D / 16 + 4 * j] : make_uint4(0, 0, 0, 0);
+      }
+      scale[r] = blk < end ? scales[blk] : 0.0f;
+    }
+  };
+  load(begin + warp * 16);
+  for (int r = warp; r < rt.count * 8; r += kWarps) {
+    const int tile = r >> 3, col = r & 7;
+    const int i = (tile >> rt.per_token << (3 - rt.group)) + (col >> rt.group);
+    const int j = (tile & rt.per_token) * 8 + (col & ((1 << rt.group) - 1));
+    const bool on = i < a.nq && j < a.gq;
+    uint2 y = make_uint2(0, 0);
+    if (on && lane < D / 4) y = *reinterpret_cast<const uint2*>(a.q + (((long long)u * a.gq + j) * a.nq + i) * D + 4 * lane);
+    const float v[4] = {bf16lo(y.x), bf16hi(y.x), bf16lo(y.y), bf16hi(y.y)};
+    const float m = warp_max_f32(fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3]))));
+    const int e = cache8_exponent<kCache8Int8>(m);
+    const float inv = two_to(-e);
+    uint32_t dn = 0, up = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int q = max(-127, min(127, __float2int_rn(v[k] * inv)));
+      dn |= ((uint32_t)min(q, 0) & 255u) << (8 * k);
+      up |= ((uint32_t)max(q, 0) & 255u) << (8 * k);
+    }
+    uint32_t* w = reinterpret_cast<uint32_t*>(sq + r * (D / 8));
+    if (lane < D / 4) w[lane] = dn, w[D / 4 + lane] = up;
+    if (lane == 0) unit[r] = on ? two_to(e) : -1.0f;
+  }
+  __syncthreads();
+  for (int at = begin + warp * 16; at < end; at += kStep) {  // warp-uniform
+    float best[4];  // (block g, columns 2c, 2c + 1), then block g + 8
+    for (int tile = 0; tile < rt.count; ++tile) {
+      int dot[4] = {0, 0, 0, 0};
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int j = 0; j < Q; ++j) {
+          const uint4 q = sq[(tile * 8 + g) * (D / 8) + s * (D / 16) + 4 * j + c];
+          imma(dot, x[0][s][j].x, x[1][s][j].x, x[0][s][j].y, x[1][s][j].y, q.x, q.y);
+          imma(dot, x[0][s][j].z, x[1][s][j].z, x[0][s][j].w, x[1][s][j].w, q.z, q.w);
+        }
+      const float2 un = *reinterpret_cast<const float2*>(unit + tile * 8 + 2 * c);
+      const float v0 = un.x > 0.0f ? (float)dot[0] * un.x : -INFINITY, v1 = un.y > 0.0f ? (float)dot[1] * un.y : -INFINITY;
+      const float v2 = un.x > 0.0f ? (float)dot[2] * un.x : -INFINITY, v3 = un.y > 0.0f ? (float)dot[3] * un.y : -INFINITY;
+      if (!(tile & rt.per_token)) {
+        best[0] = v0, best[1] = v1, best[2] = v2, best[3] = v3;
+      } else {
+        best[0] = fmaxf(best[0], v0), best[1] = fmaxf(best[1], v1), best[2] = fmaxf(best[2], v2), best[3] = fmaxf(best[3], v3);
+      }
+      if (rt.per_token && !(tile & 1)) continue;
+      // the largest of a token's columns
+      if (rt.group >= 1) best[0] = best[1] = fmaxf(best[0], best[1]), best[2] = best[3] = fmaxf(best[2], best[3]);
+      for (int o = 1; o < 1 << rt.group >> 1; o <<= 1) {
+        best[0] = fmaxf(best[0], __shfl_xor_sync(0xffffffffu, best[0], o));
+        best[2] = fmaxf(best[2], __shfl_xor_sync(0xffffffffu, best[2], o));
+      }
+      const int i0 = tile >> rt.per_token << (3 - rt.group);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {  // column 2c + k writes if it is its token's first
+        const int col = 2 * c + k, i = i0 + (col >> rt.group);
+        if ((col & ((1 << rt.group) - 1)) == 0 && i < a.nq) {
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const int blk = at + g + 8 * r;
+            const float score = best[2 * r + k] * scale[r];
+            if (blk < end) {
+              if (FUSED)
+                keys[i * per + blk - begin] = order_key(score);
+              else
+                a.scores[((long long)u * a.nq + i) * nb_max + blk] = score;
+            }
+          }
+        }
+      }
+    }
+    load(at + kStep);
+  }
+  if constexpr (FUSED) {
+    namespace cgs = cooperative_groups;
+    cgs::cluster_group cluster = cgs::this_cluster();
+    pick_prepare(sh);
+    cluster.sync();
+    uint32_t* all = keys + a.nq * per;  // [nb] where a choice among more than kPickRegs needs them all
+    const unsigned per_inv = 0xffffffffu / per + 1;  // i / per for i < 2^16, per > 1
+    for (int i = chunk; i < a.nq; i += chunks) {
+      const int seen = seen_blocks(n, a.nq, i, a.c.tb);
+      int* out = a.sel + ((long long)u * a.nq + i) * a.n_select;
+      if (seen <= a.n_select) {
+        for (int j = threadIdx.x; j < a.n_select; j += kThreads) out[j] = j < seen ? j : -1;
+        continue;
+      }
+      auto theirs = [&](int j) {
+        const int k = __umulhi((unsigned)j, per_inv);
+        return cluster.map_shared_rank(keys, k)[i * per + j - k * per];
+      };
+      if (i != chunk) {  // another token of this CTA's
+        __syncthreads();
+        pick_prepare(sh);
+      }
+      if (seen > kPickRegs)
+        for (int j = threadIdx.x; j < seen; j += kThreads) all[j] = theirs(j);
+      __syncthreads();
+      if (seen > kPickRegs)
+        pick_any([&](int j) { return all[j]; }, seen, a.n_select, a.sink, a.recent, out, sh);
+      else
+        pick_any(theirs, seen, a.n_select, a.sink, a.recent, out, sh);
+    }
+    cluster.sync();  // no CTA ends while another reads its keys
+  }
+}
+
+__global__ void __launch_bounds__(kThreads) cache8_pick_kernel(Cache8SelectArgs a, int nb_max) {
   __shared__ PickShared sh;
   const long long row = blockIdx.x;  // [nl][B][H][nq]
   const int i = (int)(row % a.nq), b = (int)(row / a.nq / a.c.k.H % a.c.k.B);
@@ -248,79 +361,90 @@ __global__ void __launch_bounds__(kPickThreads) cache8_pick_kernel(Cache8SelectA
   const int nb = seen_blocks(n, a.nq, i, a.c.tb);
   int* out = a.sel + row * a.n_select;
   if (nb <= a.n_select) {
-    for (int j = threadIdx.x; j < a.n_select; j += kPickThreads) out[j] = j < nb ? j : -1;
+    for (int j = threadIdx.x; j < a.n_select; j += kThreads) out[j] = j < nb ? j : -1;
     return;
   }
-  pick_blocks(a.scores + row * nb_max, nb, a.n_select, a.sink, a.recent, out, sh);
+  pick_prepare(sh);
+  __syncthreads();
+  const float* scores = a.scores + row * nb_max;
+  pick_any([&](int j) { return order_key(scores[j]); }, nb, a.n_select, a.sink, a.recent, out, sh);
 }
 
-__global__ void __launch_bounds__(kPickThreads) cache8_keep_kernel(Cache8EvictArgs a) {
-  __shared__ PickShared sh;
-  const int u = blockIdx.x;  // [nl][B][H]
-  const int H = a.c.k.H, B = a.c.k.B;
-  const int h = u % H, b = u / H % B, lz = u / H / B;
-  previous_kernel_done();
-  const int n = max(0, min(a.lens[b], a.c.k.T)), tb = a.c.tb, nb = (n + tb - 1) / tb;
-  const long long slice = ((long long)(a.l0 + lz) * B + b) * H + h;
+// Eviction: a CTA chooses the blocks of one (layer, batch, KV head) and moves a part of them.  The
+// choice is made again by every CTA of the unit, which costs less than a second kernel or a wait;
+// the first one writes it down.
+// LISTED: the choice (more than kListed blocks stay) has been written by cache8_keep_kernel.
+__device__ void keep_blocks(const Cache8EvictArgs& a, int u, int n, int b, int lz, int h, bool write, int* list, PickShared& sh) {
+  const int tb = a.c.tb, nb = (n + tb - 1) / tb;
+  const long long slice = ((long long)(a.l0 + lz) * a.c.k.B + b) * a.c.k.H + h;
   const float* mass = a.mass + slice * a.c.blocks();
-  float* to_mass = a.to_mass + slice * a.to.blocks();
-  int* kept = a.kept + (long long)u * a.keep;
-  if (lz == 0 && h == 0 && threadIdx.x == 0) a.to_lens[b] = nb > a.keep ? n - (nb - a.keep) * tb : n;
   if (nb <= a.keep) {
-    for (int j = threadIdx.x; j < a.keep; j += kPickThreads) kept[j] = j < nb ? j : -1;
+    for (int j = threadIdx.x; j < a.keep; j += kThreads) list[j] = j < nb ? j : -1;
   } else {
-    pick_blocks(mass, nb, a.keep, a.sink, a.recent, kept, sh);
+    pick_prepare(sh);
+    __syncthreads();
+    pick_any([&](int j) { return order_key(mass[j]); }, nb, a.keep, a.sink, a.recent, list, sh);
   }
   __syncthreads();
+  if (!write) return;
+  int* kept = a.kept + (long long)u * a.keep;
+  float* to_mass = a.to_mass + slice * a.to.blocks();
   const int m = min(nb, a.keep);
-  for (int j = threadIdx.x; j < a.to.blocks(); j += kPickThreads) to_mass[j] = j < m ? mass[kept[j]] : 0.0f;
+  if (lz == 0 && h == 0 && threadIdx.x == 0) a.to_lens[b] = nb > a.keep ? n - (nb - a.keep) * tb : n;
+  for (int j = threadIdx.x; j < a.to.blocks(); j += kThreads) to_mass[j] = j < m ? mass[list[j]] : 0.0f;
+  if (kept != list)
+    for (int j = threadIdx.x; j < a.keep; j += kThreads) kept[j] = list[j];
 }
 
-// Kept blocks of one (layer, K or V, batch, head): a warp moves 4096 bytes of codes, all its loads
-// before its stores, and what belongs to the blocks that begin there.
-__global__ void __launch_bounds__(256) cache8_move_kernel(Cache8EvictArgs a, int pieces) {
-  constexpr int kPiece = 4096;
-  const int H = a.c.k.H, B = a.c.k.B, d = a.c.k.d;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long item = (long long)blockIdx.x * 8 + warp;  // (slice, piece)
+__global__ void __launch_bounds__(kThreads) cache8_keep_kernel(Cache8EvictArgs a) {
+  __shared__ PickShared sh;
+  const unsigned H = a.c.k.H, B = a.c.k.B, u = blockIdx.x, bh = u / H;
   previous_kernel_done();
-  const int piece = (int)(item % pieces);
-  const int sl = (int)(item / pieces);
-  if (sl >= a.nl * 2 * B * H) return;
-  const int h = sl % H, b = sl / H % B, s = sl / H / B & 1, lz = sl / H / B >> 1;
-  const int* kept = a.kept + (((long long)lz * B + b) * H + h) * a.keep;
-  const long long slice = (((long long)(a.l0 + lz) * 2 + s) * B + b) * H + h;
+  const int b = bh % B;
+  keep_blocks(a, u, max(0, min(a.lens[b], a.c.k.T)), b, bh / B, u - bh * H, true, a.kept + (long long)u * a.keep, sh);
+}
+
+template <bool LISTED>
+__global__ void __launch_bounds__(kThreads, 3) cache8_evict_kernel(Cache8EvictArgs a, int parts) {
+  constexpr int kPiece = 4096;  // bytes of codes that a warp moves at a time, all loads before the stores
+  __shared__ PickShared sh;
+  extern __shared__ int s_list[];  // [keep]
+  const unsigned H = a.c.k.H, B = a.c.k.B, u = blockIdx.x / parts, bh = u / H;
+  const int part = blockIdx.x % parts, h = u - bh * H, b = bh % B, lz = bh / B;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, d = a.c.k.d;
+  const int* kept = LISTED ? a.kept + (long long)u * a.keep : s_list;
+  previous_kernel_done();
+  if (!LISTED) keep_blocks(a, u, max(0, min(a.lens[b], a.c.k.T)), b, lz, h, part == 0, s_list, sh);
   const int shift = 31 - __clz(a.c.tb * d);  // bytes of a block: 2^10 .. 2^13
-  const uint8_t* src = a.codes + slice * a.c.k.T * d;
-  uint8_t* dst = a.to_codes + slice * a.to.k.T * d;
-  uint4 v[kPiece / 512];
-  int from[kPiece / 512];
+  const int pieces = (int)((((long long)a.keep << shift) + kPiece - 1) / kPiece);  // of the keys, and of the values
+  for (int item = part * kWarps + warp; item < 2 * pieces; item += parts * kWarps) {
+    const int s = item >= pieces, piece = item - s * pieces;
+    const long long slice = (((long long)(a.l0 + lz) * 2 + s) * B + b) * H + h;
+    const uint8_t* src = a.codes + slice * a.c.k.T * d;
+    uint8_t* dst = a.to_codes + slice * a.to.k.T * d;
+    const long long p0 = (long long)piece * kPiece + 16 * lane;
+    uint4 v[kPiece / 512];
+    bool there[kPiece / 512];
 #pragma unroll
-  for (int i = 0; i < kPiece / 512; ++i) {
-    const long long at = (long long)piece * kPiece + 512 * i + 16 * lane;
-    const int j = (int)(at >> shift);
-    from[i] = j < a.keep ? kept[j] : -1;
-  }
+    for (int i = 0; i < kPiece / 512; ++i) {
+      const int j = (int)((p0 + 512 * i) >> shift), blk = j < a.keep ? kept[j] : -1;
+      there[i] = blk >= 0;
+      if (there[i]) v[i] = __ldcs(reinterpret_cast<const uint4*>(src + ((long long)blk << shift) + ((p0 + 512 * i) & ((1 << shift) - 1))));
+    }
 #pragma unroll
-  for (int i = 0; i < kPiece / 512; ++i) {
-    const long long at = (long long)piece * kPiece + 512 * i + 16 * lane;
-    if (from[i] >= 0) v[i] = __ldcs(reinterpret_cast<const uint4*>(src + ((long long)from[i] << shift) + (at & ((1 << shift) - 1))));
-  }
-#pragma unroll
-  for (int i = 0; i < kPiece / 512; ++i) {
-    const long long at = (long long)piece * kPiece + 512 * i + 16 * lane;
-    if (from[i] >= 0) *reinterpret_cast<uint4*>(dst + at) = v[i];
-  }
-  // scales and bounds of the blocks whose codes begin in the piece
-  const long long first = (((long long)piece * kPiece - 1) >> shift) + 1, last = ((long long)piece * kPiece + kPiece - 1) >> shift;
-  const long long unit = ((long long)(a.l0 + lz) * B + b) * H + h;
-  for (long long j = first; j <= last && j < a.keep; ++j) {
-    const int blk = kept[j];
-    if (blk < 0) break;
-    if (lane == 31) a.to_scales[slice * a.to.blocks() + j] = a.scales[slice * a.c.blocks() + blk];
-    if (s == 0 && a.bounds && lane < d / 8)
-      reinterpret_cast<uint4*>(a.to_bounds)[(unit * a.to.blocks() + j) * (d / 8) + lane] =
-          reinterpret_cast<const uint4*>(a.bounds)[(unit * a.c.blocks() + blk) * (d / 8) + lane];
+    for (int i = 0; i < kPiece / 512; ++i)
+      if (there[i]) *reinterpret_cast<uint4*>(dst + p0 + 512 * i) = v[i];
+    // scales and bounds of the blocks whose codes begin in the piece
+    const long long unit = ((long long)(a.l0 + lz) * B + b) * H + h;
+    const int last = (int)(((long long)piece * kPiece + kPiece - 1) >> shift);
+    for (int j = (int)((((long long)piece * kPiece - 1) >> shift) + 1); j <= last && j < a.keep; ++j) {
+      const int blk = kept[j];
+      if (blk < 0) break;
+      if (lane == 31) a.to_scales[slice * a.to.blocks() + j] = a.scales[slice * a.c.blocks() + blk];
+      if (s == 0 && a.bounds && lane < d / 8)
+        reinterpret_cast<uint4*>(a.to_bounds)[(unit * a.to.blocks() + j) * (d / 8) + lane] =
+            reinterpret_cast<const uint4*>(a.bounds)[(unit * a.c.blocks() + blk) * (d / 8) + lane];
+    }
   }
 }
 
@@ -328,44 +452,73 @@ namespace {
 
 long long select_units(const Cache8SelectArgs& a) { return (long long)a.nl * a.c.k.B * a.c.k.H; }
 int select_nb(const Cache8SelectArgs& a) { return (a.max_tokens + a.c.tb - 1) / a.c.tb; }
-// blocks that a CTA scores: enough CTAs for the GPU, but up to eight times kScoreBlocks each, so that
-// the query rows are rounded for many blocks
-int score_per(const Cache8SelectArgs& a) {
-  const long long want = (select_units(a) * select_nb(a) + 8 * kSms - 1) / (8 * kSms);
-  const long long steps = (want + kScoreBlocks - 1) / kScoreBlocks;
-  return kScoreBlocks * (int)(steps > 8 ? 8 : steps);
+bool select_fused(const Cache8SelectArgs& a) { return select_nb(a) <= kPickKeys; }
+// CTAs of a unit.  Fused: a cluster of up to eight, no more than the GPU holds at once beyond two
+// unless the keys of all query tokens would not fit.  Else as many as keep the rows' rounding to one
+// in eight steps.
+int score_chunks(const Cache8SelectArgs& a) {
+  const int steps = (select_nb(a) + kStep - 1) / kStep;
+  if (!select_fused(a)) return (steps + 7) / 8;
+  int c = 1;
+  while (c < 8 && c < steps && (c < 2 || select_units(a) * c * 2 <= 5 * kSms || (long long)a.nq * select_nb(a) / c > 8192)) c *= 2;
+  return c;
 }
-int score_chunks(const Cache8SelectArgs& a) { return (select_nb(a) + score_per(a) - 1) / score_per(a); }
-int move_pieces(const Cache8EvictArgs& a) { return (int)(((long long)a.keep * a.c.tb * a.c.k.d + 4095) / 4096); }
-long long move_ctas(const Cache8EvictArgs& a) { return ((long long)a.nl * 2 * a.c.k.B * a.c.k.H * move_pieces(a) + 7) / 8; }
+int score_per(const Cache8SelectArgs& a) {
+  const int c = score_chunks(a);
+  return ((select_nb(a) + c - 1) / c + 15) / 16 * 16;
+}
+size_t score_smem(const Cache8SelectArgs& a) {
+  const RowTiles rt = row_tiles(a.gq, a.nq);
+  return (size_t)rt.count * 8 * (2 * a.c.k.d + sizeof(float)) + (select_fused(a) ? (size_t)a.nq * score_per(a) * 4 : 0) +
+         (select_fused(a) && select_nb(a) > kPickRegs ? (size_t)select_nb(a) * 4 : 0);
+}
+long long evict_units(const Cache8EvictArgs& a) { return (long long)a.nl * a.c.k.B * a.c.k.H; }
+// CTAs of a unit: enough for the GPU, but at least 64 KB of codes to move for each choice made
+int evict_parts(const Cache8EvictArgs& a) {
+  const long long bytes = 2LL * a.keep * a.c.tb * a.c.k.d, most = (bytes + 65535) / 65536;
+  const long long want = (4 * kSms + evict_units(a) - 1) / evict_units(a);
+  return (int)(want < most ? want : most);
+}
+bool evict_listed(const Cache8EvictArgs& a) { return a.keep > kListed; }
 
 }  // namespace
 
 uint64_t cache8_select_workspace(const Cache8SelectArgs& a) {
-  return ((uint64_t)select_units(a) * a.nq * select_nb(a) * sizeof(float) + 15) & ~15ull;
+  return select_fused(a) ? 16 : ((uint64_t)select_units(a) * a.nq * select_nb(a) * sizeof(float) + 15) & ~15ull;
 }
 bool cache8_select_fits(const Cache8SelectArgs& a) {
   return select_units(a) * score_chunks(a) < (1LL << 31) && select_units(a) * a.nq < (1LL << 31);
 }
 cudaError_t launch_cache8_select(const Cache8SelectArgs& a, cudaStream_t st) {
-  const int rows = a.gq * a.nq, d = a.c.k.d, per = score_per(a), chunks = score_chunks(a), nb = select_nb(a);
-  const size_t smem = (size_t)rows * (2 * d + sizeof(float)), most = (size_t)kMaxGroup * kMaxQTokens * (2 * d + sizeof(float));
-  static std::atomic<uint64_t> ready[2];
-  auto kern = d == 128 ? cache8_score_kernel<128> : cache8_score_kernel<64>;
-  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), most, ready[d == 128]);
+  const int chunks = score_chunks(a), per = score_per(a), nb = select_nb(a);
+  const bool fused = select_fused(a), wide = a.c.k.d == 128;
+  static std::atomic<uint64_t> ready[4];
+  auto kern = fused ? (wide ? cache8_score_kernel<128, true> : cache8_score_kernel<64, true>)
+                    : (wide ? cache8_score_kernel<128, false> : cache8_score_kernel<64, false>);
+  // 256 rows of 256 bytes, the keys of 16 tokens and 1024 blocks, and those of one token and all
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), 176 * 1024, ready[2 * fused + wide]);
   if (e != cudaSuccess) return e;
-  e = launch_after(kern, dim3((unsigned)(select_units(a) * chunks)), kScoreThreads, smem, st, 1, a, chunks, per, nb);
-  if (e != cudaSuccess) return e;
-  return launch_after(cache8_pick_kernel, dim3((unsigned)(select_units(a) * a.nq)), kPickThreads, 0, st, 1, a, nb);
+  e = launch_after(kern, dim3((unsigned)(select_units(a) * chunks)), kThreads, score_smem(a), st, fused ? chunks : 1, a, chunks, per, nb);
+  if (e != cudaSuccess || fused) return e;
+  return launch_after(cache8_pick_kernel, dim3((unsigned)(select_units(a) * a.nq)), kThreads, 0, st, 1, a, nb);
 }
 
 bool cache8_evict_fits(const Cache8EvictArgs& a) {
-  return move_ctas(a) < (1LL << 31) && (long long)a.nl * 2 * a.c.k.B * a.c.k.H < (1LL << 31);
+  const long long most = (1LL << 31) - 1;
+  return evict_units(a) * evict_parts(a) <= most && ((long long)a.keep * a.c.tb * a.c.k.d + 4095) / 4096 <= most / 2;
 }
 cudaError_t launch_cache8_evict(const Cache8EvictArgs& a, cudaStream_t st) {
-  const cudaError_t e = launch_after(cache8_keep_kernel, dim3((unsigned)(a.nl * a.c.k.B * a.c.k.H)), kPickThreads, 0, st, 1, a);
+  const int parts = evict_parts(a);
+  const unsigned ctas = (unsigned)(evict_units(a) * parts);
+  if (!evict_listed(a)) {
+    static std::atomic<uint64_t> ready;
+    const cudaError_t e = allow_smem(reinterpret_cast<const void*>(cache8_evict_kernel<false>), kListed * 4, ready);
+    if (e != cudaSuccess) return e;
+    return launch_after(cache8_evict_kernel<false>, dim3(ctas), kThreads, a.keep * sizeof(int), st, 1, a, parts);
+  }
+  const cudaError_t e = launch_after(cache8_keep_kernel, dim3((unsigned)evict_units(a)), kThreads, 0, st, 1, a);
   if (e != cudaSuccess) return e;
-  return launch_after(cache8_move_kernel, dim3((unsigned)move_ctas(a)), 256, 0, st, 1, a, move_pieces(a));
+  return launch_after(cache8_evict_kernel<true>, dim3(ctas), kThreads, 0, st, 1, a, parts);
 }
 
 }  // namespace cg

@@ -122,7 +122,8 @@ def test_select_refuses(over):
 def test_select_pointers_and_workspace():
     sd = cg.cache8_select_desc(8, 500, 8, q_tokens=3)
     need = cg.cg_cache8_select_workspace_size(KV, C8, sd)
-    assert need >= 4 * 3 * 2 * 3 * 32
+    long_kv = cg.kv_desc(1, 3, 2, 1 << 18, 64)                                # scores beyond a CTA's memory
+    assert cg.cg_cache8_select_workspace_size(long_kv, C8, cg.cache8_select_desc(8, 1 << 18, 8, q_tokens=3)) == 4 * 3 * 2 * 3 * (1 << 14)
     assert _select(sd, bytes_=need - 1) == cg.CG_ERR_INVALID
     for bad in (dict(q=0), dict(scales=0), dict(bounds=0), dict(lens=0), dict(sel=0), dict(ws=0), dict(bounds=0x3004), dict(sel=0x5004)):
         assert _select(sd, **bad) == cg.CG_ERR_INVALID

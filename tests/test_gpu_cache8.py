@@ -328,17 +328,19 @@ def test_select_matches_the_definition(code, d, tb, gq, nq, k, sink, recent):
     assert np.array_equal(got, o8.select(bf16_np(q), c.bounds, c.scales, lens, tb, k, sink, recent, H, layer0=1))
 
 
-def test_select_among_many_blocks():
+@pytest.mark.parametrize("T,d,nq,ks", [(32768, 64, 1, (1, 100, 1500, 2047)), (131072, 64, 16, (77,)), (163840, 128, 2, (1, 9000))])
+def test_select_among_many_blocks(T, d, nq, ks):
+    """Up to 8192 blocks are chosen in one kernel (for 16 query tokens too), more in two."""
     need_gpu()
-    T, d, tb = 32768, 64, 16
+    tb = 16
     rng = np.random.default_rng(0)
     c = Cache(1, 2, 1, T, d, cg.CACHE8_INT8, tb)
     b = np.sort(rng.integers(-127, 128, c.bounds.shape).astype(np.int8), axis=4)
     c.bounds = np.ascontiguousarray(b)
     c.scales = (2.0 ** rng.integers(-4, 4, c.scales.shape)).astype(np.float32)
     c.up()
-    q = _new(torch.Generator().manual_seed(1), 1, 2, 4, 1, d)
-    for k in (1, 100, 1500, 2047):
+    q = _new(torch.Generator().manual_seed(1), 1, 2, 4, nq, d)
+    for k in ks:
         lens = [T, T - 4000]
         assert np.array_equal(_select(c, q, lens, k, 0, 1), o8.select(bf16_np(q), c.bounds, c.scales, lens, tb, k, 0, 1, 1))
 
@@ -390,15 +392,16 @@ def test_evict_matches_the_definition(code, d, tb, keep, sink, recent, T2, bound
     assert np.array_equal(to.d_mass.cpu().numpy(), to.mass, equal_nan=True)
 
 
-def test_evict_from_many_blocks():
+@pytest.mark.parametrize("T,keep", [(40960, 1000), (163840, 9000)])
+def test_evict_from_many_blocks(T, keep):
     need_gpu()
-    L, B, H, T, d, tb, keep = 1, 1, 2, 40960, 64, 16, 1000
+    L, B, H, d, tb = 1, 1, 2, 64, 16
     c = Cache(L, B, H, T, d, cg.CACHE8_INT8, tb)
     rng = np.random.default_rng(3)
     c.scales = np.ones_like(c.scales)
     c.mass = rng.integers(0, 300, c.mass.shape).astype(np.float32)   # many ties
     c.up()
-    to = Cache(L, B, H, 16000, d, cg.CACHE8_INT8, tb)
+    to = Cache(L, B, H, keep * tb, d, cg.CACHE8_INT8, tb)
     tl = np.zeros(B, np.int32)
     d_tl, kept = _cuda(tl), torch.empty((1, B, H, keep), dtype=torch.int32, device="cuda")
     cg.cg_cache8_evict(c.kv, c.c8, cg.cache8_evict_desc(keep, 3, 5), _cuda(np.array([T - 9], np.int32)), c.d_codes, c.d_scales, c.d_bounds, c.d_mass,
