@@ -380,14 +380,15 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm(D, NT)) cache8_attn_k
           }
       }
       uint32_t bhi[NT][2], blo[NT][2];
+      float tile_sum[2 * NT];  // of this lane's two tokens: column (nt, j)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        float pv[4], tile_sum[2];
+        float pv[4];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const float p0 = ex2(x[nt][j]), p1 = ex2(x[nt][j + 2]);
-          tile_sum[j] = p0 + p1;
-          l_run[nt][j] += tile_sum[j];
+          tile_sum[2 * nt + j] = p0 + p1;
+          l_run[nt][j] += tile_sum[2 * nt + j];
           // p s_V relative to M': p 2^f <= 2^(kLag + kShift), so a factor of over 2^100 meets a p below 2^-85, whose
           // row's sum holds a weight of 1 at least: nothing that a result in fp32 could show
           const float f = ex2(fminf((vexp + kShift) - mv_m[nt][j], 100.0f));
@@ -401,15 +402,31 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm(D, NT)) cache8_attn_k
           bhi[nt][j] = transpose_8x8(*reinterpret_cast<const uint32_t*>(&hi));
           blo[nt][j] = transpose_8x8(*reinterpret_cast<const uint32_t*>(&lo));
         }
-        if (MASS) {
+      }
+      if (MASS) {
+        // over the eight lanes of a column, each step halving the columns that a lane keeps: lane g
+        // ends with one
+        float ref[2 * NT];
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const float sum = column_sum(tile_sum[j]);
-            const int r = rt * R + nt * 8 + 2 * c + j;
-            if (g == 0 && r < rows)
-              a.tile_mass[(first + r) * ((a.max_tokens + 15) >> 4) + (tile0 + warp + i * kWarps)] = make_float2(sum, m_run[nt][j]);
+        for (int k = 0; k < 2 * NT; ++k) ref[k] = m_run[k >> 1][k & 1];
+        int o = 4;
+#pragma unroll
+        for (int half = NT; half >= 1; half >>= 1, o <<= 1) {
+          const bool up = lane & o;
+#pragma unroll
+          for (int k = 0; k < half; ++k) {
+            const float keep = up ? tile_sum[half + k] : tile_sum[k], give = up ? tile_sum[k] : tile_sum[half + k];
+            tile_sum[k] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+            ref[k] = up ? ref[half + k] : ref[k];
           }
         }
+#pragma unroll
+        for (; o <= 16; o <<= 1) tile_sum[0] += __shfl_xor_sync(0xffffffffu, tile_sum[0], o);
+        // the column that the halving left: its high bit was decided first
+        const int col = NT == 2 ? (g & 1) * 2 + (g >> 1 & 1) : g & 1;
+        const int r = rt * R + (col >> 1) * 8 + 2 * c + (col & 1);
+        if (g < 2 * NT && r < rows)
+          a.tile_mass[(first + r) * ((a.max_tokens + 15) >> 4) + (tile0 + warp + i * kWarps)] = make_float2(tile_sum[0], ref[0]);
       }
       // o[channel][row] += codes^T p
 #pragma unroll
@@ -624,13 +641,13 @@ void plan(Cache8AttnArgs& a) {
   a.ctas = (int)(runs < most ? runs : most);
   // clusters: as many CTAs as give each warp one tile of the longest unit, where the GPU holds them
   // all at once.  A unit that is shorter than the others leaves its CTAs idle, so no warp may get
-  // more than kClusterTiles, unless all units are of one length (one sequence) and fill the GPU:
-  // there 32 layers of 1024 (2048, 4096) tokens took 18.2 (27.9, 48.1) us, with equal runs and the
-  // second kernel 24.3 (33.5, 50.9).
+  // more than kClusterTiles, unless all units are of one length (one sequence, or lists) and fill the
+  // GPU: there 32 layers of 1024 (2048, 4096) tokens took 18.2 (27.9, 48.1) us, with equal runs and
+  // the second kernel 24.3 (33.5, 50.9).
   const long long unit = a.n_select ? (long long)a.n_select * (a.c.tb / 16) : (a.max_tokens + 15) / 16;
   int size = 1;
   while (size < kMaxCluster && size * kWarps < unit && units(a) * size * 2 <= most) size *= 2;
-  const bool even = a.c.k.B == 1 && a.nq == 1 && 4 * units(a) * size >= 3 * most;
+  const bool even = (a.c.k.B == 1 || a.n_select) && 4 * units(a) * size >= 3 * most;
   a.cluster = units(a) <= most && (even || unit <= (long long)size * kWarps * kClusterTiles) ? size : 0;
   if (a.cluster) a.ctas = (int)units(a) * size;
 }

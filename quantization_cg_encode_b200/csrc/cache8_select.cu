@@ -213,8 +213,9 @@ __host__ __device__ inline RowTiles row_tiles(int gq, int nq) {
 
 // A CTA scores `per` blocks of one (layer, batch, KV head).  FUSED: the CTAs of a cluster share the
 // unit, each keeps its scores as keys, and the choice follows; else the scores go to a.scores.
-template <int D, bool FUSED>
-__global__ void __launch_bounds__(kThreads, 4) cache8_score_kernel(Cache8SelectArgs a, int chunks, int per, int nb_max) {
+// CTAS: how many of them an SM has to hold.
+template <int D, bool FUSED, int CTAS>
+__global__ void __launch_bounds__(kThreads, CTAS) cache8_score_kernel(Cache8SelectArgs a, int chunks, int per, int nb_max) {
   constexpr int Q = D / 64;               // 16-byte pieces of a lane, of one bound of one block
   __shared__ PickShared sh;
   extern __shared__ uint4 sq[];           // [tile][column][q8 <= 0, q8 >= 0][D / 16]
@@ -492,11 +493,15 @@ bool cache8_select_fits(const Cache8SelectArgs& a) {
 cudaError_t launch_cache8_select(const Cache8SelectArgs& a, cudaStream_t st) {
   const int chunks = score_chunks(a), per = score_per(a), nb = select_nb(a);
   const bool fused = select_fused(a), wide = a.c.k.d == 128;
-  static std::atomic<uint64_t> ready[4];
-  auto kern = fused ? (wide ? cache8_score_kernel<128, true> : cache8_score_kernel<64, true>)
-                    : (wide ? cache8_score_kernel<128, false> : cache8_score_kernel<64, false>);
+  static std::atomic<uint64_t> ready[6];
+  // Two CTAs an SM leave registers for all loads at once, four the more CTAs: one sequence of 2048
+  // blocks and its attention took 16.4 us with two and 18.2 with four, 32 sequences 74.8 and 71.9.
+  const bool many = fused && select_units(a) * chunks > 2 * kSms;
+  auto kern = many ? (wide ? cache8_score_kernel<128, true, 4> : cache8_score_kernel<64, true, 4>)
+              : fused ? (wide ? cache8_score_kernel<128, true, 2> : cache8_score_kernel<64, true, 2>)
+                      : (wide ? cache8_score_kernel<128, false, 2> : cache8_score_kernel<64, false, 2>);
   // 256 rows of 256 bytes, the keys of 16 tokens and 1024 blocks, and those of one token and all
-  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), 176 * 1024, ready[2 * fused + wide]);
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), 176 * 1024, ready[2 * (fused + many) + wide]);
   if (e != cudaSuccess) return e;
   e = launch_after(kern, dim3((unsigned)(select_units(a) * chunks)), kThreads, score_smem(a), st, fused ? chunks : 1, a, chunks, per, nb);
   if (e != cudaSuccess || fused) return e;
