@@ -68,7 +68,7 @@ __device__ __forceinline__ uint32_t as_u32(__nv_bfloat162 v) { return *reinterpr
 constexpr uint32_t kBf16Inf2 = 0x7F807F80u, kBf16NegInf2 = 0xFF80FF80u;
 
 template <int D, int CODE>
-__global__ void __launch_bounds__(kWarps * 32) append_kernel(Cache8AppendArgs a, unsigned window, int tb_shift) {
+__global__ void __launch_bounds__(kWarps * 32, 8) append_kernel(Cache8AppendArgs a, unsigned window, int tb_shift) {
   constexpr int LPT = D / 8;         // lanes a token
   constexpr int TPL = 32 / LPT;      // tokens a warp loads at once: 2 or 4
   constexpr int NL = 16 / TPL;       // loads of a warp

@@ -406,7 +406,7 @@ __global__ void __launch_bounds__(kThreads) cache8_keep_kernel(Cache8EvictArgs a
 }
 
 template <bool LISTED>
-__global__ void __launch_bounds__(kThreads, 3) cache8_evict_kernel(Cache8EvictArgs a, int parts) {
+__global__ void __launch_bounds__(kThreads, 4) cache8_evict_kernel(Cache8EvictArgs a, int parts) {
   constexpr int kPiece = 4096;  // bytes of codes that a warp moves at a time, all loads before the stores
   __shared__ PickShared sh;
   extern __shared__ int s_list[];  // [keep]
