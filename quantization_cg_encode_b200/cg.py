@@ -374,11 +374,15 @@ def alloc_cache8(kvd, c8, device="cuda"):
             torch.zeros((L, B, H, nb), dtype=torch.float32, device=device))
 
 
+# These calls are made once a layer and token: what their checks cost is a large part of a short call.
+
+
 def _cache8_counts(kvd, c8):
-    """What cg_cache8_sizes_for gives, without a call of the library (these calls are made once a layer
-    and token); a block size that the library refuses counts as one token."""
-    heads, T, d = kvd.layers * kvd.batch * kvd.heads, kvd.tokens, kvd.d_head
-    blocks = heads * (T // (c8.tb if c8.tb > 0 else 1))
+    """(bytes of codes, scales, bytes of bounds, entries of mass) as cg_cache8_sizes_for gives them, without
+    a call of the library; a block size that the library refuses counts as one token."""
+    T, d, tb = kvd.tokens, kvd.d_head, c8.tb
+    heads = kvd.layers * kvd.batch * kvd.heads
+    blocks = heads * (T // tb if tb > 0 else T)
     return 2 * heads * T * d, 2 * blocks, 2 * blocks * d, blocks
 
 
@@ -386,10 +390,17 @@ def _at(t, dtype, name, numel, dev):
     """Address of a contiguous tensor of the given dtype on CUDA device `dev` (None -> NULL)."""
     if t is None:
         return None
-    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev >= 0 and t.is_contiguous() and t.numel() >= numel:
-        return t.data_ptr()
+    try:
+        if t.dtype is dtype and t.get_device() == dev and t.is_contiguous() and t.numel() >= numel and dev >= 0:
+            return t.data_ptr()
+    except AttributeError:
+        pass
     _ptr(t, dtype, name, numel)  # says what is wrong with it
     raise ValueError("%s is on cuda:%d, another tensor of the call on cuda:%d" % (name, t.get_device(), dev))
+
+
+def _device_of(t):
+    return t.get_device() if isinstance(t, torch.Tensor) else -1
 
 
 def _here(stream, dev):
@@ -412,14 +423,14 @@ def cg_cache8_append(kvd, c8, layer0, new, pos, counts, codes, scales, bounds, s
     """Append new bf16 [n_layers, 2, B, H, n, d] at positions pos int32 [B]; of the n tokens sequence
     b takes counts[b] (int32 [B], None: all); bounds may be None."""
     cb, sc, bb, _ = _cache8_counts(kvd, c8)
-    B, dev = kvd.batch, codes.get_device()
+    B, dev = kvd.batch, _device_of(codes)
     shape = new.shape
     if len(shape) != 6 or shape[1] != 2 or shape[2] != B or shape[3] != kvd.heads or shape[5] != kvd.d_head:
         raise ValueError("new must be [n_layers, 2, %d, %d, n, %d], got %s" % (B, kvd.heads, kvd.d_head, tuple(shape)))
     if new.numel() == 0:
         return
     status = lib().cg_cache8_append(
-        ctypes.byref(kvd), ctypes.byref(c8), layer0, shape[0], shape[4], _at(new, torch.bfloat16, "new", 1, dev),
+        kvd, c8, layer0, shape[0], shape[4], _at(new, torch.bfloat16, "new", 1, dev),
         _at(pos, torch.int32, "pos", B, dev), _at(counts, torch.int32, "counts", B, dev),
         _at(codes, torch.uint8, "codes", cb, dev), _at(scales, torch.float32, "scales", sc, dev),
         _at(bounds, torch.int8, "bounds", bb, dev), _here(stream, dev))
@@ -439,11 +450,11 @@ def cg_cache8_attention(kvd, c8, at, q, codes, scales, lens, out, workspace, sel
     out fp32 of the same shape; sel int32 [n_layers, B, H, q_tokens, n_select] restricts it to listed
     blocks; mass fp32 [L, B, H, T/tb] receives every block's softmax weight."""
     cb, sc, _, mc = _cache8_counts(kvd, c8)
-    B, dev = kvd.batch, codes.get_device()
+    B, dev = kvd.batch, _device_of(codes)
     rows = at.n_layers * B * at.q_tokens
     nq = rows * at.q_heads * kvd.d_head
     status = lib().cg_cache8_attention(
-        ctypes.byref(kvd), ctypes.byref(c8), ctypes.byref(at), _at(q, torch.bfloat16, "q", nq, dev),
+        kvd, c8, at, _at(q, torch.bfloat16, "q", nq, dev),
         _at(codes, torch.uint8, "codes", cb, dev), _at(scales, torch.float32, "scales", sc, dev),
         _at(lens, torch.int32, "lens", B, dev), _at(sel, torch.int32, "sel", rows * kvd.heads * at.n_select, dev),
         _at(out, torch.float32, "out", nq, dev), _at(mass, torch.float32, "mass", mc, dev),
@@ -463,10 +474,10 @@ def cg_cache8_select(kvd, c8, sd, q, scales, bounds, lens, sel, workspace, strea
     """The n_select blocks of each KV head and query token whose bounds promise the largest scores:
     q bf16 [n_layers, B, Hq, q_tokens, d] -> sel int32 [n_layers, B, H, q_tokens, n_select]."""
     _, sc, bb, _ = _cache8_counts(kvd, c8)
-    B, dev = kvd.batch, bounds.get_device()
+    B, dev = kvd.batch, _device_of(bounds)
     rows = sd.n_layers * B * sd.q_tokens
     status = lib().cg_cache8_select(
-        ctypes.byref(kvd), ctypes.byref(c8), ctypes.byref(sd),
+        kvd, c8, sd,
         _at(q, torch.bfloat16, "q", rows * sd.q_heads * kvd.d_head, dev), _at(scales, torch.float32, "scales", sc, dev),
         _at(bounds, torch.int8, "bounds", bb, dev), _at(lens, torch.int32, "lens", B, dev),
         _at(sel, torch.int32, "sel", rows * kvd.heads * sd.n_select, dev), _at(workspace, torch.uint8, "workspace", 1, dev),
@@ -481,11 +492,11 @@ def cg_cache8_evict(kvd, c8, ev, lens, codes, scales, bounds, mass, to_kvd, to_c
     both be None); kept int32 [n_layers, B, H, keep_blocks] receives their indices."""
     cb, sc, bb, mc = _cache8_counts(kvd, c8)
     tcb, tsc, tbb, tmc = _cache8_counts(to_kvd, c8)
-    B, dev = kvd.batch, codes.get_device()
+    B, dev = kvd.batch, _device_of(codes)
     status = lib().cg_cache8_evict(
-        ctypes.byref(kvd), ctypes.byref(c8), ctypes.byref(ev), _at(lens, torch.int32, "lens", B, dev),
+        kvd, c8, ev, _at(lens, torch.int32, "lens", B, dev),
         _at(codes, torch.uint8, "codes", cb, dev), _at(scales, torch.float32, "scales", sc, dev),
-        _at(bounds, torch.int8, "bounds", bb, dev), _at(mass, torch.float32, "mass", mc, dev), ctypes.byref(to_kvd),
+        _at(bounds, torch.int8, "bounds", bb, dev), _at(mass, torch.float32, "mass", mc, dev), to_kvd,
         _at(to_codes, torch.uint8, "to_codes", tcb, dev), _at(to_scales, torch.float32, "to_scales", tsc, dev),
         _at(to_bounds, torch.int8, "to_bounds", tbb, dev), _at(to_mass, torch.float32, "to_mass", tmc, dev),
         _at(to_lens, torch.int32, "to_lens", B, dev),
