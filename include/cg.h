@@ -338,8 +338,8 @@ cg_status cg_decode_attention(const cg_kv_desc* kv, const cg_codec_desc* codec, 
  * length counts as clamped to [0, max_tokens], and what lies beyond is not read.
  * Nothing needs clearing before use except `mass`.  Every call works on the layers
  * [layer0, layer0 + n_layers) of the cache; its inputs and outputs other than the
- * cache hold only those.  Requests of more than 2^31 - 1 query rows or thread
- * blocks return CG_ERR_TOO_LARGE.  Results do not depend on timing (no floating-point atomics). */
+ * cache hold only those.  Requests of more than 2^31 - 1 query rows, thread
+ * blocks or 16-token tiles return CG_ERR_TOO_LARGE.  Results do not depend on timing (no floating-point atomics). */
 typedef enum {
   CG_CACHE8_INT8 = 0, /* codes -127 .. 127 */
   CG_CACHE8_E4M3 = 1  /* codes -448 .. 448, four bits of exponent and three of mantissa */

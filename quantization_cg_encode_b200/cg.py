@@ -391,7 +391,7 @@ def _at(t, dtype, name, numel, dev):
     if t is None:
         return None
     try:
-        if t.dtype is dtype and t.get_device() == dev and t.is_contiguous() and t.numel() >= numel and dev >= 0:
+        if t.dtype is dtype and t.get_device() == dev and t.is_contiguous() and t.numel() >= numel:
             return t.data_ptr()
     except AttributeError:
         pass
@@ -399,8 +399,11 @@ def _at(t, dtype, name, numel, dev):
     raise ValueError("%s is on cuda:%d, another tensor of the call on cuda:%d" % (name, t.get_device(), dev))
 
 
-def _device_of(t):
-    return t.get_device() if isinstance(t, torch.Tensor) else -1
+def _device_of(t, name):
+    """CUDA device of a call by one of its tensors."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError("%s must be a CUDA tensor" % name)
+    return t.get_device()
 
 
 def _here(stream, dev):
@@ -423,12 +426,12 @@ def cg_cache8_append(kvd, c8, layer0, new, pos, counts, codes, scales, bounds, s
     """Append new bf16 [n_layers, 2, B, H, n, d] at positions pos int32 [B]; of the n tokens sequence
     b takes counts[b] (int32 [B], None: all); bounds may be None."""
     cb, sc, bb, _ = _cache8_counts(kvd, c8)
-    B, dev = kvd.batch, _device_of(codes)
-    shape = new.shape
+    B, shape = kvd.batch, new.shape
     if len(shape) != 6 or shape[1] != 2 or shape[2] != B or shape[3] != kvd.heads or shape[5] != kvd.d_head:
         raise ValueError("new must be [n_layers, 2, %d, %d, n, %d], got %s" % (B, kvd.heads, kvd.d_head, tuple(shape)))
     if new.numel() == 0:
         return
+    dev = _device_of(codes, "codes")
     status = lib().cg_cache8_append(
         kvd, c8, layer0, shape[0], shape[4], _at(new, torch.bfloat16, "new", 1, dev),
         _at(pos, torch.int32, "pos", B, dev), _at(counts, torch.int32, "counts", B, dev),
@@ -450,7 +453,7 @@ def cg_cache8_attention(kvd, c8, at, q, codes, scales, lens, out, workspace, sel
     out fp32 of the same shape; sel int32 [n_layers, B, H, q_tokens, n_select] restricts it to listed
     blocks; mass fp32 [L, B, H, T/tb] receives every block's softmax weight."""
     cb, sc, _, mc = _cache8_counts(kvd, c8)
-    B, dev = kvd.batch, _device_of(codes)
+    B, dev = kvd.batch, _device_of(codes, "codes")
     rows = at.n_layers * B * at.q_tokens
     nq = rows * at.q_heads * kvd.d_head
     status = lib().cg_cache8_attention(
@@ -474,7 +477,7 @@ def cg_cache8_select(kvd, c8, sd, q, scales, bounds, lens, sel, workspace, strea
     """The n_select blocks of each KV head and query token whose bounds promise the largest scores:
     q bf16 [n_layers, B, Hq, q_tokens, d] -> sel int32 [n_layers, B, H, q_tokens, n_select]."""
     _, sc, bb, _ = _cache8_counts(kvd, c8)
-    B, dev = kvd.batch, _device_of(bounds)
+    B, dev = kvd.batch, _device_of(bounds, "bounds")
     rows = sd.n_layers * B * sd.q_tokens
     status = lib().cg_cache8_select(
         kvd, c8, sd,
@@ -492,7 +495,7 @@ def cg_cache8_evict(kvd, c8, ev, lens, codes, scales, bounds, mass, to_kvd, to_c
     both be None); kept int32 [n_layers, B, H, keep_blocks] receives their indices."""
     cb, sc, bb, mc = _cache8_counts(kvd, c8)
     tcb, tsc, tbb, tmc = _cache8_counts(to_kvd, c8)
-    B, dev = kvd.batch, _device_of(codes)
+    B, dev = kvd.batch, _device_of(codes, "codes")
     status = lib().cg_cache8_evict(
         kvd, c8, ev, _at(lens, torch.int32, "lens", B, dev),
         _at(codes, torch.uint8, "codes", cb, dev), _at(scales, torch.float32, "scales", sc, dev),

@@ -710,7 +710,7 @@ uint64_t cache8_attn_workspace(Cache8AttnArgs a, bool want_mass) {
 bool cache8_attn_fits(Cache8AttnArgs a, bool want_mass) {
   const long long most = (1LL << 31) - 1;
   plan(a);
-  return tiles_of(a) <= most && total_rows(a) <= most && (!want_mass || (long long)a.nl * a.c.k.B * a.c.k.H * mass_chunks(a) <= most);
+  return tiles_of(a) <= most - (1 << 16) && total_rows(a) <= most && (!want_mass || (long long)a.nl * a.c.k.B * a.c.k.H * mass_chunks(a) <= most);
 }
 
 cudaError_t launch_cache8_attention(Cache8AttnArgs a, void* workspace, cudaStream_t st) {

@@ -67,16 +67,15 @@ static_assert(kThreads == 256, "four histograms of 64 words of 16 bytes");
 // Radix selection finds the key of the last one taken, eight bits a pass from the first bit in
 // which the keys differ, until few keys are left, which are counted against one another; then one
 // ordered pass writes the list.  Every warp reads the histogram for itself: one barrier a pass.
-// A thread has KPT consecutive keys in registers, at(i) gives key i (KPT 0: a run of them, read
-// each time).
-template <int KPT, typename At>
-__device__ void pick_blocks(At at, int nb, int k, int sink, int recent, int* out, PickShared& sh) {
+// A thread has KPT consecutive keys in registers (keys.load gives them, of whatever stands behind
+// the last one), keys(i) gives key i (KPT 0: a run of them, read each time).
+template <int KPT, typename Keys>
+__device__ void pick_blocks(const Keys& keys, int nb, int k, int sink, int recent, int* out, PickShared& sh) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int lo = sink, hi = nb - recent;
   uint32_t u[KPT ? KPT : 1];
   if constexpr (KPT > 0) {
-#pragma unroll
-    for (int j = 0; j < KPT; ++j) u[j] = tid * KPT + j < nb ? at(tid * KPT + j) : 0;
+    if (tid * KPT < nb) keys.load(tid * KPT, nb, u);
   }
   auto each = [&](auto f) {
     if constexpr (KPT > 0) {
@@ -86,7 +85,7 @@ __device__ void pick_blocks(At at, int nb, int k, int sink, int recent, int* out
         if (i >= lo && i < hi) f(u[j]);
       }
     } else {
-      for (int i = lo + tid; i < hi; i += kThreads) f(at(i));
+      for (int i = lo + tid; i < hi; i += kThreads) f(keys(i));
     }
   };
   uint32_t least = 0xffffffffu, most = 0;
@@ -160,7 +159,7 @@ __device__ void pick_blocks(At at, int nb, int k, int sink, int recent, int* out
       for (int j = 0; j < KPT; ++j)
         if (tid * KPT + j < nb) f(tid * KPT + j, kind(tid * KPT + j, u[j]));
     } else {
-      for (int i = i0; i < i1; ++i) f(i, kind(i, at(i)));
+      for (int i = i0; i < i1; ++i) f(i, kind(i, keys(i)));
     }
   };
   uint32_t sure = 0, equal = 0;
@@ -184,15 +183,53 @@ __device__ void pick_blocks(At at, int nb, int k, int sink, int recent, int* out
     }
   });
 }
-template <typename At>
-__device__ __forceinline__ void pick_any(At at, int nb, int k, int sink, int recent, int* out, PickShared& sh) {
+template <typename Keys>
+__device__ __forceinline__ void pick_any(const Keys& keys, int nb, int k, int sink, int recent, int* out, PickShared& sh) {
   if (nb <= 2 * kThreads)
-    pick_blocks<2>(at, nb, k, sink, recent, out, sh);
+    pick_blocks<2>(keys, nb, k, sink, recent, out, sh);
   else if (nb <= kPickRegs)
-    pick_blocks<8>(at, nb, k, sink, recent, out, sh);
+    pick_blocks<8>(keys, nb, k, sink, recent, out, sh);
   else
-    pick_blocks<0>(at, nb, k, sink, recent, out, sh);
+    pick_blocks<0>(keys, nb, k, sink, recent, out, sh);
 }
+// Keys of fp32 values in global memory
+struct ValueKeys {
+  const float* v;
+  __device__ uint32_t operator()(int i) const { return order_key(v[i]); }
+  template <int N>
+  __device__ void load(int i, int nb, uint32_t (&u)[N]) const {
+    float x[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) x[j] = i + j < nb ? v[i + j] : 0.0f;
+#pragma unroll
+    for (int j = 0; j < N; ++j) u[j] = order_key(x[j]);
+  }
+};
+// Keys that the CTAs of a cluster hold, `per` (a multiple of 16) each
+struct ClusterKeys {
+  const uint32_t* mine;
+  int per;
+  unsigned per_inv;  // i / per = umulhi(i, per_inv) for i < 2^16
+  __device__ const uint32_t* of(int i) const {
+    const int k = __umulhi((unsigned)i, per_inv);
+    return cooperative_groups::this_cluster().map_shared_rank(mine, k) + (i - k * per);
+  }
+  __device__ uint32_t operator()(int i) const { return *of(i); }
+  __device__ void load(int i, int, uint32_t (&u)[2]) const {
+    const uint2 x = *reinterpret_cast<const uint2*>(of(i));
+    u[0] = x.x, u[1] = x.y;
+  }
+  __device__ void load(int i, int, uint32_t (&u)[8]) const {
+    const uint4* p = reinterpret_cast<const uint4*>(of(i));
+    const uint4 x = p[0], y = p[1];
+    u[0] = x.x, u[1] = x.y, u[2] = x.z, u[3] = x.w, u[4] = y.x, u[5] = y.y, u[6] = y.z, u[7] = y.w;
+  }
+};
+// Keys in this CTA's shared memory
+struct HeldKeys {
+  const uint32_t* v;
+  __device__ uint32_t operator()(int i) const { return v[i]; }
+};
 
 // Query rows in tiles of eight operand columns: up to eight heads make a group of 1, 2, 4 or 8
 // columns, as many query tokens to a tile as fit; more heads take two tiles a token.
@@ -333,21 +370,22 @@ __global__ void __launch_bounds__(kThreads, CTAS) cache8_score_kernel(Cache8Sele
         for (int j = threadIdx.x; j < a.n_select; j += kThreads) out[j] = j < seen ? j : -1;
         continue;
       }
-      auto theirs = [&](int j) {
-        const int k = __umulhi((unsigned)j, per_inv);
-        return cluster.map_shared_rank(keys, k)[i * per + j - k * per];
-      };
+      const ClusterKeys theirs{keys + i * per, per, per_inv};
       if (i != chunk) {  // another token of this CTA's
         __syncthreads();
         pick_prepare(sh);
       }
-      if (seen > kPickRegs)
+      if (seen > kPickRegs) {
+#pragma unroll 4
         for (int j = threadIdx.x; j < seen; j += kThreads) all[j] = theirs(j);
+      }
       __syncthreads();
       if (seen > kPickRegs)
-        pick_any([&](int j) { return all[j]; }, seen, a.n_select, a.sink, a.recent, out, sh);
+        pick_blocks<0>(HeldKeys{all}, seen, a.n_select, a.sink, a.recent, out, sh);
+      else if (seen > 2 * kThreads)
+        pick_blocks<8>(theirs, seen, a.n_select, a.sink, a.recent, out, sh);
       else
-        pick_any(theirs, seen, a.n_select, a.sink, a.recent, out, sh);
+        pick_blocks<2>(theirs, seen, a.n_select, a.sink, a.recent, out, sh);
     }
     cluster.sync();  // no CTA ends while another reads its keys
   }
@@ -367,8 +405,7 @@ __global__ void __launch_bounds__(kThreads) cache8_pick_kernel(Cache8SelectArgs 
   }
   pick_prepare(sh);
   __syncthreads();
-  const float* scores = a.scores + row * nb_max;
-  pick_any([&](int j) { return order_key(scores[j]); }, nb, a.n_select, a.sink, a.recent, out, sh);
+  pick_any(ValueKeys{a.scores + row * nb_max}, nb, a.n_select, a.sink, a.recent, out, sh);
 }
 
 // Eviction: a CTA chooses the blocks of one (layer, batch, KV head) and moves a part of them.  The
@@ -384,7 +421,7 @@ __device__ void keep_blocks(const Cache8EvictArgs& a, int u, int n, int b, int l
   } else {
     pick_prepare(sh);
     __syncthreads();
-    pick_any([&](int j) { return order_key(mass[j]); }, nb, a.keep, a.sink, a.recent, list, sh);
+    pick_any(ValueKeys{mass}, nb, a.keep, a.sink, a.recent, list, sh);
   }
   __syncthreads();
   if (!write) return;

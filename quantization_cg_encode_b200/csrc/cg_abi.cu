@@ -375,6 +375,6 @@ const char* cg_status_string(cg_status s) {
   return "unknown status";
 }
 
-int32_t cg_version(void) { return 100; }
+int32_t cg_version(void) { return 200; }
 
 }  // extern "C"

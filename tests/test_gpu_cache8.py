@@ -182,14 +182,33 @@ def test_attention_lengths_and_groups(code, d, tb, gq, nq):
 
 
 @pytest.mark.parametrize("code", [cg.CACHE8_INT8, cg.CACHE8_E4M3])
-@pytest.mark.parametrize("B,T,gq,nq", [(1, 8192, 4, 1), (3, 2048, 4, 4), (1, 5120, 1, 1)])
-def test_attention_splits(code, B, T, gq, nq):
-    """Long sequences that several CTAs share, with value scales 2^40 apart and far tokens that matter."""
+@pytest.mark.parametrize("B,T,gq,nq", [(1, 8192, 4, 1), (3, 2048, 4, 4), (1, 5120, 1, 1), (2, 24576, 3, 1), (3, 17408, 4, 4)])
+def test_attention_of_long_sequences(code, B, T, gq, nq):
+    """Sequences that the CTAs of a cluster share, or (over 16384 tokens) that equal runs cut into
+    many pieces, with value scales 2^40 apart and far tokens that matter."""
     need_gpu()
     lens = [T - 3 - 700 * b for b in range(B)]
+    if T > 16384:
+        lens[1] = 0                     # a vacant sequence between or behind long ones
     c = _filled(1, B, 1, T, 64, code, 16, lens, seed=T, spread=40)
     q = _new(torch.Generator().manual_seed(2), 1, B, gq, nq, 64, gain=4.0)
     _check_attention(c, q, lens, max_tokens=T - 1)
+
+
+@pytest.mark.parametrize("d,gq,nq", [(128, 2, 1), (64, 3, 4)])
+def test_attention_runs_over_many_ragged_sequences_with_block_weights(d, gq, nq):
+    """More units than CTAs: a CTA's run holds whole sequences and pieces of two more."""
+    need_gpu()
+    B, H, T = 45, 8, 256
+    lens = [(97 * b) % (T + 1) for b in range(B)]
+    c = _filled(1, B, H, T, d, cg.CACHE8_INT8, 32, lens, seed=d)
+    q = _new(torch.Generator().manual_seed(d), 1, B, H * gq, nq, d, gain=1.5)
+    ref, want, spread, big = _check_attention(c, q, lens)
+    eps = big.max() * (d / 16 + 4) * 2.0 ** -23 + 40 * 2.0 ** -22
+    mass = torch.full((1, B, H, T // 32), 7.0, dtype=torch.float32, device="cuda")
+    got = _attend(c, q, lens, mass=mass)
+    _close(got, ref, spread, big, d)
+    assert np.all(np.abs(mass.cpu().numpy().astype(np.float64) - want) <= 2 * eps * want)
 
 
 def test_attention_batch_of_many_heads_takes_whole_sequences_a_cta():
@@ -261,13 +280,26 @@ def test_attention_over_listed_blocks(code, d, tb, gq, nq, k):
     _check_attention(c, q, lens, sel=sel)
 
 
-def test_attention_over_a_long_list():
+@pytest.mark.parametrize("T,tb,k", [(8192, 16, 300), (32768, 64, 300)])
+def test_attention_over_a_long_list(T, tb, k):
+    """One list for a cluster, and one (1200 tiles) for equal runs."""
     need_gpu()
-    T, d, tb, k = 8192, 64, 16, 300
+    d = 64
     c = _filled(1, 1, 1, T, d, cg.CACHE8_INT8, tb, [T - 5], seed=21)
     sel = np.random.default_rng(1).permutation(T // tb)[:k].reshape(1, 1, 1, 1, k)
     q = _new(torch.Generator().manual_seed(9), 1, 1, 2, 1, d, gain=2.0)
     _check_attention(c, q, [T - 5], sel=sel)
+
+
+def test_attention_over_lists_of_many_ragged_sequences():
+    need_gpu()
+    B, H, T, d, tb, k, nq = 30, 4, 512, 64, 16, 9, 3
+    lens = [(61 * b) % (T + 1) for b in range(B)]
+    c = _filled(1, B, H, T, d, cg.CACHE8_E4M3, tb, lens, seed=22)
+    q = _new(torch.Generator().manual_seed(10), 1, B, 2 * H, nq, d)
+    sel = _select(c, q, lens, k, 1, 1)
+    assert np.array_equal(sel, o8.select(bf16_np(q), c.bounds, c.scales, lens, tb, k, 1, 1, H))
+    _check_attention(c, q, lens, sel=sel)
 
 
 def test_attention_behind_four_gigabytes():
@@ -410,6 +442,38 @@ def test_evict_from_many_blocks(T, keep):
     want = o8.evict(c.codes, c.scales, c.bounds, c.mass, [T - 9], (to.codes, to.scales, to.bounds, to.mass, tl), tb, keep, 3, 5)
     assert np.array_equal(kept.cpu().numpy(), want) and d_tl.item() == tl[0]
     to.same()
+
+
+# ---- the binding -----------------------------------------------------------------------------------
+
+
+def test_binding_refuses_before_a_launch(monkeypatch):
+    need_gpu()
+    c = _filled(1, 1, 1, 64, 64, cg.CACHE8_INT8, 16, [40])
+    at = cg.cache8_attn_desc(2, 64, d_head=64)
+    ws = torch.empty(cg.cg_cache8_attention_workspace_size(c.kv, c.c8, at), dtype=torch.uint8, device="cuda")
+    q, lens = torch.zeros((1, 1, 2, 1, 64), dtype=torch.bfloat16, device="cuda"), torch.tensor([40], dtype=torch.int32, device="cuda")
+    out = torch.full(q.shape, 3.0, device="cuda")
+
+    def call(q=q, lens=lens, out=out, ws=ws, codes=c.d_codes, scales=c.d_scales, **more):
+        return cg.cg_cache8_attention(c.kv, c.c8, at, q, codes, scales, lens, out, ws, **more)
+
+    for error, bad in ((TypeError, dict(q=q.float())), (TypeError, dict(lens=lens.long())), (TypeError, dict(lens=lens.cpu())),
+                       (TypeError, dict(codes=[1])), (ValueError, dict(out=out[..., :32])), (ValueError, dict(q=q[:, :, :, :, ::2])),
+                       (ValueError, dict(scales=c.d_scales[..., :2].contiguous())), (cg.CgError, dict(ws=ws[:16])),
+                       (cg.CgError, dict(sel=torch.zeros(4, dtype=torch.int32, device="cuda"))), (TypeError, dict(mass=c.d_codes)),
+                       (cg.CgError, dict(lens=torch.zeros(8, dtype=torch.int32, device="cuda")[1:]))):
+        with pytest.raises(error):
+            call(**bad)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)   # the tensors lie on another device
+    with pytest.raises(ValueError):
+        call()
+    monkeypatch.undo()
+    cg.cg_sync_status()
+    assert bool((out == 3.0).all())
+    call()
+    cg.cg_sync_status()
+    assert not bool((out == 3.0).any())
 
 
 # ---- together ----------------------------------------------------------------------------------------
