@@ -597,12 +597,24 @@ __global__ void __launch_bounds__(256) cache8_mass_kernel(Cache8AttnArgs a, int 
   const int i0 = blk * tpb, i1 = min(live, i0 + tpb);
   float sum = 0.0f;
   if (i0 < i1) {
-    for (int r = warp; r < rows; r += 8) {
-      const float2 st = a.stats[u * rows + r];
-      const float2* tm = a.tile_mass + (u * rows + r) * tiles;
-      float part = 0.0f;
-      for (int i = i0; i < i1; ++i) part = __fmaf_rn(tm[i].x, ex2(tm[i].y - st.x), part);
-      sum = __fmaf_rn(part, st.y, sum);
+    // four rows' loads together
+    for (int r = warp; r < rows; r += 32) {
+      float2 st[4], tm[4][4];  // a block has four tiles at most
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const bool on = r + 8 * k < rows;
+        const float2* row = a.tile_mass + (u * rows + (on ? r + 8 * k : r)) * tiles;
+        st[k] = on ? a.stats[u * rows + r + 8 * k] : make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tm[k][i] = i0 + i < i1 ? row[i0 + i] : make_float2(0.0f, kNone);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float part = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) part = __fmaf_rn(tm[k][i].x, ex2(fminf(tm[k][i].y - st[k].x, kLag)), part);
+        sum = __fmaf_rn(part, st[k].y, sum);
+      }
     }
   }
   s_sum[warp][lane] = sum;
