@@ -73,7 +73,8 @@ __global__ void __launch_bounds__(kWarps * 32, 8) append_kernel(Cache8AppendArgs
   constexpr int TPL = 32 / LPT;      // tokens a warp loads at once: 2 or 4
   constexpr int NL = 16 / TPL;       // loads of a warp
   __shared__ float s_max[kWarps];
-  __shared__ float s_lo[kWarps][D], s_hi[kWarps][D];  // extremes of the code values
+  __shared__ uint4 s_ext[kWarps][LPT][2];         // extremes of the new tokens, bf16 pairs: low, high
+  __shared__ float s_old[kWarps][2][D];           // and of the code values of older tokens rounded anew
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int wpb = 1 << (tb_shift - 4);                // warps of a block: 1, 2 or 4
   // (slice, block of the window: the blocks that n tokens touch at most)
@@ -137,18 +138,12 @@ __global__ void __launch_bounds__(kWarps * 32, 8) append_kernel(Cache8AppendArgs
     for (int i = 0; i < NL; ++i)
       if (fresh >> i & 1u) widen(x[i]);
   }
-#pragma unroll
-  for (int o = LPT; o < 32; o <<= 1)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      lo[j] = __hmin2(lo[j], as_bf16x2(__shfl_xor_sync(0xffffffffu, as_u32(lo[j]), o)));
-      hi[j] = __hmax2(hi[j], as_bf16x2(__shfl_xor_sync(0xffffffffu, as_u32(hi[j]), o)));
-    }
-  float m = 0.0f;  // (a lane without new tokens has -inf and inf: no maximum)
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float2 l2 = __bfloat1622float2(lo[j]), h2 = __bfloat1622float2(hi[j]);
-    if (l2.x <= h2.x) m = fmaxf(fmaxf(m, fmaxf(fabsf(l2.x), fabsf(h2.x))), fmaxf(fabsf(l2.y), fabsf(h2.y)));
+  float m = 0.0f;
+  if (fresh) {  // (a lane without new tokens has inf and -inf)
+    const __nv_bfloat162 x0 = __hmax2(__hmax2(__habs2(lo[0]), __habs2(hi[0])), __hmax2(__habs2(lo[1]), __habs2(hi[1])));
+    const __nv_bfloat162 x1 = __hmax2(__hmax2(__habs2(lo[2]), __habs2(hi[2])), __hmax2(__habs2(lo[3]), __habs2(hi[3])));
+    const float2 f = __bfloat1622float2(__hmax2(x0, x1));
+    m = fmaxf(f.x, f.y);
   }
   m = warp_max_f32(m);
   if (wpb > 1) {
@@ -178,64 +173,76 @@ __global__ void __launch_bounds__(kWarps * 32, 8) append_kernel(Cache8AppendArgs
       if (fresh >> i & 1u) to[i * 32] = coded(x[i]);
   }
   const bool keys = a.bounds != nullptr && s == 0;
-  // code values of the extremes, by the same rounding
-  float vlo[8], vhi[8];
-  if (keys || grew) {
+  if (keys) {
 #pragma unroll
-    for (int j = 0; j < 4; j += 2) {
-      const float2 l0 = __bfloat1622float2(lo[j]), l1 = __bfloat1622float2(lo[j + 1]);
-      const float2 h0 = __bfloat1622float2(hi[j]), h1 = __bfloat1622float2(hi[j + 1]);
-      float v[4];
-      unpack_codes<CODE>(pack_codes<CODE>(l0.x * inv, l0.y * inv, l1.x * inv, l1.y * inv), v);
+    for (int o = LPT; o < 32; o <<= 1)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) vlo[2 * j + k] = l0.x <= h0.x ? v[k] : 448.0f;
-      unpack_codes<CODE>(pack_codes<CODE>(h0.x * inv, h0.y * inv, h1.x * inv, h1.y * inv), v);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) vhi[2 * j + k] = l0.x <= h0.x ? v[k] : -448.0f;
-    }
-  }
-  if (grew) {  // the block's older codes, rounded anew
-    for (int t = t0; t < min(pos, first + 16); t += TPL) {
-      uint2* at = reinterpret_cast<uint2*>(row + (long long)t * D);
-      uint2 c = *at;
-      float v[8];
-      unpack_codes<CODE>(c.x, *reinterpret_cast<float(*)[4]>(v));
-      unpack_codes<CODE>(c.y, *reinterpret_cast<float(*)[4]>(v + 4));
-      c.x = pack_codes<CODE>(v[0] * ratio, v[1] * ratio, v[2] * ratio, v[3] * ratio);
-      c.y = pack_codes<CODE>(v[4] * ratio, v[5] * ratio, v[6] * ratio, v[7] * ratio);
-      *at = c;
-      unpack_codes<CODE>(c.x, *reinterpret_cast<float(*)[4]>(v));
-      unpack_codes<CODE>(c.y, *reinterpret_cast<float(*)[4]>(v + 4));
-#pragma unroll
-      for (int j = 0; j < 8; ++j) vlo[j] = fminf(vlo[j], v[j]), vhi[j] = fmaxf(vhi[j], v[j]);
-    }
-  }
-  if (__syncthreads_or(keys && (wpb > 1 || grew))) {  // extremes that lie in several lanes or warps
-    if (keys) {
-#pragma unroll
-      for (int o = LPT; o < 32; o <<= 1)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          vlo[j] = fminf(vlo[j], __shfl_xor_sync(0xffffffffu, vlo[j], o));
-          vhi[j] = fmaxf(vhi[j], __shfl_xor_sync(0xffffffffu, vhi[j], o));
-        }
-      if (sub == 0) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) s_lo[warp][ch + j] = vlo[j], s_hi[warp][ch + j] = vhi[j];
+      for (int j = 0; j < 4; ++j) {
+        lo[j] = __hmin2(lo[j], as_bf16x2(__shfl_xor_sync(0xffffffffu, as_u32(lo[j]), o)));
+        hi[j] = __hmax2(hi[j], as_bf16x2(__shfl_xor_sync(0xffffffffu, as_u32(hi[j]), o)));
       }
+    if (wpb > 1 && sub == 0) {
+      s_ext[warp][lane][0] = make_uint4(as_u32(lo[0]), as_u32(lo[1]), as_u32(lo[2]), as_u32(lo[3]));
+      s_ext[warp][lane][1] = make_uint4(as_u32(hi[0]), as_u32(hi[1]), as_u32(hi[2]), as_u32(hi[3]));
+    }
+  }
+  if (__syncthreads_or(grew)) {  // the older codes of a block, rounded anew (every warp has read its scale)
+    float vlo[8], vhi[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) vlo[j] = 448.0f, vhi[j] = -448.0f;
+    if (grew) {
+      for (int t = t0; t < min(pos, first + 16); t += TPL) {
+        uint2* at = reinterpret_cast<uint2*>(row + (long long)t * D);
+        uint2 c = *at;
+        float v[8];
+        unpack_codes<CODE>(c.x, *reinterpret_cast<float(*)[4]>(v));
+        unpack_codes<CODE>(c.y, *reinterpret_cast<float(*)[4]>(v + 4));
+        c.x = pack_codes<CODE>(v[0] * ratio, v[1] * ratio, v[2] * ratio, v[3] * ratio);
+        c.y = pack_codes<CODE>(v[4] * ratio, v[5] * ratio, v[6] * ratio, v[7] * ratio);
+        *at = c;
+        unpack_codes<CODE>(c.x, *reinterpret_cast<float(*)[4]>(v));
+        unpack_codes<CODE>(c.y, *reinterpret_cast<float(*)[4]>(v + 4));
+#pragma unroll
+        for (int j = 0; j < 8; ++j) vlo[j] = fminf(vlo[j], v[j]), vhi[j] = fmaxf(vhi[j], v[j]);
+      }
+    }
+#pragma unroll
+    for (int o = LPT; o < 32; o <<= 1)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        vlo[j] = fminf(vlo[j], __shfl_xor_sync(0xffffffffu, vlo[j], o));
+        vhi[j] = fmaxf(vhi[j], __shfl_xor_sync(0xffffffffu, vhi[j], o));
+      }
+    if (sub == 0) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s_old[warp][0][ch + j] = vlo[j], s_old[warp][1][ch + j] = vhi[j];
     }
     __syncthreads();
-    if (keys && part == 0) {
-      for (int i = 1; i < wpb; ++i) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) vlo[j] = fminf(vlo[j], s_lo[warp + i][ch + j]), vhi[j] = fmaxf(vhi[j], s_hi[warp + i][ch + j]);
-      }
-    }
   }
-  // (every warp of the block has read the old scale before the barrier above)
   if (live && part == 0) {
     if (lane == 0) *sp = two_to(e);
     if (keys && sub == 0) {
+      for (int i = 1; i < wpb; ++i) {
+        const uint4 l = s_ext[warp + i][lane][0], h4 = s_ext[warp + i][lane][1];
+        const uint32_t lw[4] = {l.x, l.y, l.z, l.w}, hw[4] = {h4.x, h4.y, h4.z, h4.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) lo[j] = __hmin2(lo[j], as_bf16x2(lw[j])), hi[j] = __hmax2(hi[j], as_bf16x2(hw[j]));
+      }
+      // their code values, by the same rounding
+      float vlo[8], vhi[8];
+#pragma unroll
+      for (int j = 0; j < 4; j += 2) {
+        const float2 l0 = __bfloat1622float2(lo[j]), l1 = __bfloat1622float2(lo[j + 1]);
+        const float2 h0 = __bfloat1622float2(hi[j]), h1 = __bfloat1622float2(hi[j + 1]);
+        unpack_codes<CODE>(pack_codes<CODE>(l0.x * inv, l0.y * inv, l1.x * inv, l1.y * inv), *reinterpret_cast<float(*)[4]>(vlo + 2 * j));
+        unpack_codes<CODE>(pack_codes<CODE>(h0.x * inv, h0.y * inv, h1.x * inv, h1.y * inv), *reinterpret_cast<float(*)[4]>(vhi + 2 * j));
+      }
+      if (grew) {
+        for (int i = 0; i < wpb; ++i) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) vlo[j] = fminf(vlo[j], s_old[warp + i][0][ch + j]), vhi[j] = fmaxf(vhi[j], s_old[warp + i][1][ch + j]);
+        }
+      }
       const long long unit = ((long long)(a.l0 + lz) * a.c.k.B + b) * a.c.k.H + h;
       uint2* at = reinterpret_cast<uint2*>(a.bounds + (unit * a.c.blocks() + blk) * 2 * D + ch);
       int l8[8], h8[8];
