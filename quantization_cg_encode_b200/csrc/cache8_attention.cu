@@ -11,7 +11,8 @@
 //   scores  A = 16 tokens x 16 channels of key codes, exact in fp16; B = q, times a power of two
 //           per row that puts its largest element into [2^14, 2^15): bf16 values are exact in
 //           fp16 down to 2^-29 of the row's largest;
-//   values  A = 16 channels x 16 tokens of value codes; B = p as two fp16 terms (2^-22).
+//   values  A = 16 channels x 16 tokens of value codes; B = p as two fp16 terms (2^-22), which are
+//           two products, or, for up to four rows (PAIR), columns 0-3 and 4-7 of one.
 // The order of channels within a contraction is free, so ldmatrix moves the bytes as 16-bit
 // pairs and no thread exchanges codes with another; B of the second product is the scores'
 // layout transposed (movmatrix).
@@ -115,7 +116,7 @@ struct Tail {
 
 }  // namespace
 
-template <int D, int CODE, int NT, bool SPARSE, bool MASS>
+template <int D, int CODE, int NT, bool PAIR, bool SPARSE, bool MASS>
 __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm(D, NT)) cache8_attn_kernel(Cache8AttnArgs a) {
   constexpr int R = 8 * NT, CH = D / 16, TILE = 16 * D;  // CH: 16-byte pieces of a row
   __shared__ float s_m[kWarps][R], s_mv[kWarps][R], s_l[kWarps][R];
@@ -360,7 +361,7 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm(D, NT)) cache8_attn_k
           }
           x[nt][j] = __fmaf_rn(s[nt][j], factor[nt][j], -m_run[nt][j]);
           x[nt][j + 2] = __fmaf_rn(s[nt][j + 2], factor[nt][j], -m_run[nt][j]);
-          over |= fmaxf(x[nt][j], x[nt][j + 2]) > fminf(kLag, mv_m[nt][j] + (kLag - vexp));
+          over |= (!PAIR || c < 2) && fmaxf(x[nt][j], x[nt][j + 2]) > fminf(kLag, mv_m[nt][j] + (kLag - vexp));
         }
       if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
@@ -370,7 +371,11 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm(D, NT)) cache8_attn_k
             const float top = column_max(fmaxf(s[nt][j], s[nt][j + 2])) * factor[nt][j];
             const float m_old = m_run[nt][j], mv_old = mv_run[nt][j];
             const float m = fmaxf(m_old, top), mv = fmaxf(mv_old, top + vexp);
-            const float fv = ex2(mv_old - mv);
+            float fv = ex2(mv_old - mv);
+            if (PAIR) {  // columns 4-7 go with 0-3
+              const float other = __shfl_xor_sync(0xffffffffu, fv, 2);
+              fv = c < 2 ? fv : other;
+            }
             m_run[nt][j] = m, mv_run[nt][j] = mv, mv_m[nt][j] = mv - m;
             l_run[nt][j] *= ex2(m_old - m);
             x[nt][j] = __fmaf_rn(s[nt][j], factor[nt][j], -m);
@@ -399,8 +404,13 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm(D, NT)) cache8_attn_k
           const __half2 hi = __floats2half2_rn(pv[2 * j], pv[2 * j + 1]);
           const float2 back = __half22float2(hi);
           const __half2 lo = __floats2half2_rn(pv[2 * j] - back.x, pv[2 * j + 1] - back.y);
-          bhi[nt][j] = transpose_8x8(*reinterpret_cast<const uint32_t*>(&hi));
-          blo[nt][j] = transpose_8x8(*reinterpret_cast<const uint32_t*>(&lo));
+          if (PAIR) {
+            const uint32_t other = __shfl_xor_sync(0xffffffffu, *reinterpret_cast<const uint32_t*>(&lo), 2);
+            bhi[nt][j] = transpose_8x8(c < 2 ? *reinterpret_cast<const uint32_t*>(&hi) : other);
+          } else {
+            bhi[nt][j] = transpose_8x8(*reinterpret_cast<const uint32_t*>(&hi));
+            blo[nt][j] = transpose_8x8(*reinterpret_cast<const uint32_t*>(&lo));
+          }
         }
       }
       if (MASS) {
@@ -442,7 +452,7 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm(D, NT)) cache8_attn_k
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             mma_f16_16816(o[nt][2 * jj + k], af, bhi[nt][0], bhi[nt][1]);
-            mma_f16_16816(o[nt][2 * jj + k], af, blo[nt][0], blo[nt][1]);
+            if (!PAIR) mma_f16_16816(o[nt][2 * jj + k], af, blo[nt][0], blo[nt][1]);
           }
         }
       }
@@ -488,7 +498,11 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm(D, NT)) cache8_attn_k
       float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        const float4 v = *reinterpret_cast<const float4*>(&s_o[(w * R + r) * D + ch]);
+        float4 v = *reinterpret_cast<const float4*>(&s_o[(w * R + r) * D + ch]);
+        if (PAIR) {
+          const float4 lo = *reinterpret_cast<const float4*>(&s_o[(w * R + r + 4) * D + ch]);
+          v.x += lo.x, v.y += lo.y, v.z += lo.z, v.w += lo.w;
+        }
         const float f = s_w[w][r];
         acc.x = __fmaf_rn(v.x, f, acc.x), acc.y = __fmaf_rn(v.y, f, acc.y), acc.z = __fmaf_rn(v.z, f, acc.z), acc.w = __fmaf_rn(v.w, f, acc.w);
       }
@@ -682,28 +696,29 @@ void layout(Cache8AttnArgs& a, char* base, bool want_mass, uint64_t& bytes) {
   bytes = at;
 }
 
-template <int D, int CODE, int NT, bool SPARSE, bool MASS>
+template <int D, int CODE, int NT, bool PAIR, bool SPARSE, bool MASS>
 cudaError_t launch_one(const Cache8AttnArgs& a, cudaStream_t st) {
   const size_t tiles = (size_t)kWarps * kStages * 32 * D, outputs = sizeof(float) * 8 * NT * (kWarps * D + D + 4);
   const size_t smem = tiles > outputs ? tiles : outputs;
-  auto kern = cache8_attn_kernel<D, CODE, NT, SPARSE, MASS>;
+  auto kern = cache8_attn_kernel<D, CODE, NT, PAIR, SPARSE, MASS>;
   static std::atomic<uint64_t> ready{0};  // a bit a device
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), smem, ready);
   if (e != cudaSuccess) return e;
   return launch_after(kern, dim3(a.ctas), kWarps * 32, smem, st, a.cluster, a);
 }
-template <int D, int CODE, int NT>
+template <int D, int CODE, int NT, bool PAIR>
 cudaError_t launch_kind(const Cache8AttnArgs& a, cudaStream_t st) {
-  if (a.n_select) return launch_one<D, CODE, NT, true, false>(a, st);
-  return a.mass ? launch_one<D, CODE, NT, false, true>(a, st) : launch_one<D, CODE, NT, false, false>(a, st);
+  if (a.n_select) return launch_one<D, CODE, NT, PAIR, true, false>(a, st);
+  return a.mass ? launch_one<D, CODE, NT, PAIR, false, true>(a, st) : launch_one<D, CODE, NT, PAIR, false, false>(a, st);
+}
+template <int D, int CODE>
+cudaError_t launch_rows(const Cache8AttnArgs& a, cudaStream_t st) {
+  if (a.nt == 2) return launch_kind<D, CODE, 2, false>(a, st);
+  return (a.n_select ? a.gq : a.gq * a.nq) <= 4 ? launch_kind<D, CODE, 1, true>(a, st) : launch_kind<D, CODE, 1, false>(a, st);
 }
 template <int D>
 cudaError_t launch_d(const Cache8AttnArgs& a, cudaStream_t st) {
-  cudaError_t e;
-  if (a.c.code == kCache8Int8)
-    e = a.nt == 1 ? launch_kind<D, kCache8Int8, 1>(a, st) : launch_kind<D, kCache8Int8, 2>(a, st);
-  else
-    e = a.nt == 1 ? launch_kind<D, kCache8E4m3, 1>(a, st) : launch_kind<D, kCache8E4m3, 2>(a, st);
+  const cudaError_t e = a.c.code == kCache8Int8 ? launch_rows<D, kCache8Int8>(a, st) : launch_rows<D, kCache8E4m3>(a, st);
   if (e != cudaSuccess || a.cluster) return e;
   return launch_after(cache8_combine_kernel<D>, dim3(a.ctas, 8 * a.nt), D, 0, st, 1, a, a.mass != nullptr);
 }
