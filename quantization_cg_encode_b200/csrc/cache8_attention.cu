@@ -29,6 +29,12 @@
 // A unit that lies in one run goes out as it is; the pieces of the others go to the workspace
 // and a second kernel merges them.  Where units are few and short, a cluster of CTAs takes each
 // instead and merges through its shared memory: no looking for a place, no second kernel.
+//
+// Measured (B200, d = 128, 4 query heads a KV head): 32 layers x 8 heads of 4096 tokens, int8,
+// 48 us = 5.6 TB/s; 64 ragged sequences of up to 8192 tokens, e4m3, 114 us = 5.9 TB/s.  A tile costs
+// 377 instructions of a warp, of which the codes' conversion is 174 (int8) and products 16.  With
+// 16 rows the products (48 a tile) and the other 460 instructions share the issue slots, which
+// bound it: 32 rows, 12 sequences of up to 16001 tokens, 71 us with block weights, 1.7 TB/s.
 #include <cooperative_groups.h>
 
 #include "cache8.cuh"

