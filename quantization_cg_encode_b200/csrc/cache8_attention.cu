@@ -105,11 +105,18 @@ __device__ __forceinline__ float column_sum(float v) {
   return v;
 }
 __device__ __forceinline__ int clamped_len(const Cache8AttnArgs& a, int b) { return max(0, min(a.lens[b], a.max_tokens)); }
-// 16-token tiles of a unit: all that it may see, or all that are listed
-__device__ __forceinline__ int unit_tiles(const Cache8AttnArgs& a, int b) {
-  const int n = clamped_len(a, b);
+// 16-token tiles of a unit of a sequence of n tokens: all that it may see, or all that are listed
+__device__ __forceinline__ int unit_tiles(const Cache8AttnArgs& a, int n) {
   return a.n_select ? (n ? a.n_select * (a.c.tb >> 4) : 0) : (n + 15) >> 4;
 }
+
+// A unit, its first tile in this CTA, and the CTA's run
+struct Place {
+  int lz, b, idx, n;             // layer of the call, sequence, unit of the two, tokens of the sequence
+  int tile0, tiles;              // first tile, tiles of the unit
+  int unit_at;                   // the unit's first tile in the row of all tiles
+  int begin, end, run;
+};
 
 // A unit whose last piece is in this CTA's run and whose first is not
 struct Tail {
@@ -128,6 +135,7 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm(D, NT)) cache8_attn_k
   __shared__ float s_m[kWarps][R], s_mv[kWarps][R], s_l[kWarps][R];
   __shared__ float s_w[kWarps][R], s_fin[R][3];
   __shared__ float s_scale[kWarps][kStages][2];
+  __shared__ Place s_place;
   // the warps' tiles [kWarps][kStages][key, value][TILE], then their outputs fp32 [kWarps][R][D]
   extern __shared__ __align__(128) unsigned char dyn[];
   float* s_o = reinterpret_cast<float*>(dyn);
@@ -148,65 +156,73 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm(D, NT)) cache8_attn_k
   previous_kernel_done();
   dependents_may_launch();
 
-  int lz = 0, b = 0, idx = 0, tile0 = 0, tiles = 0;
-  int unit_at = 0;  // the unit's first tile in the row of all tiles
-  int begin = 0, end_all, run = 1;
-  if (a.cluster) {  // a cluster is a unit: an equal part of its tiles to every CTA
-    const int unit = blockIdx.x / a.cluster, rank = blockIdx.x % a.cluster;
-    idx = unit % per_batch, b = unit / per_batch % B, lz = unit / per_batch / B;
-    tiles = unit_tiles(a, b);
-    const int part = (tiles + a.cluster - 1) / a.cluster;
-    begin = tile0 = min(tiles, rank * part);
-    end_all = min(tiles, begin + part);
-    float* mine = s_part;
-    if (begin == end_all && a.cluster > 1)  // a piece without weight
-      for (int e = tid; e < R * (D + 4); e += kWarps * 32) mine[e] = e % (D + 4) < 2 ? kNone : 0.0f;
-  } else {
-    // The run of this CTA in the row of all tiles, and the unit in which it begins: every warp sums
-    // the batch's tiles for itself, 32 sequences at a time, and finds the place on a second way.
-    int batch_tiles = 0;  // of one unit of every sequence
-    for (int b0 = lane; b0 < B; b0 += 32) batch_tiles += unit_tiles(a, b0);
-    batch_tiles = __reduce_add_sync(0xffffffffu, batch_tiles);
-    const int layer_tiles = batch_tiles * per_batch, total = layer_tiles * a.nl;
-    run = max(kLeastRun, (total + (int)gridDim.x - 1) / (int)gridDim.x);
-    begin = (int)min((long long)total, (long long)blockIdx.x * run);
-    end_all = min(total, begin + run);
-    const bool any = begin < end_all;
-    lz = any ? begin / layer_tiles : 0;
-    const int rem = begin - lz * layer_tiles;
-    int passed = 0;
-    for (int b0 = 0; any; b0 += 32) {
-      const int v = b0 + lane < B ? unit_tiles(a, b0 + lane) * per_batch : 0;
-      int incl = v;
+  // Where the CTA begins: found by one warp and taken from shared memory by all, so that lengths
+  // that change meanwhile (they should not) cannot part the threads of a CTA.
+  if (warp == 0) {
+    Place p = {0, 0, 0, 0, 0, 0, 0, 0, 0, 1};
+    if (a.cluster) {  // a cluster is a unit: an equal part of its tiles to every CTA
+      const int unit = blockIdx.x / a.cluster, rank = blockIdx.x % a.cluster;
+      p.idx = unit % per_batch, p.b = unit / per_batch % B, p.lz = unit / per_batch / B;
+      p.n = clamped_len(a, p.b);
+      p.tiles = unit_tiles(a, p.n);
+      const int part = (p.tiles + a.cluster - 1) / a.cluster;
+      p.begin = p.tile0 = min(p.tiles, rank * part);
+      p.end = min(p.tiles, p.begin + part);
+    } else {
+      // The run in the row of all tiles, and the unit in which it begins: the warp sums the batch's
+      // tiles, 32 sequences at a time, and finds the place on a second way.
+      int batch_tiles = 0;  // of one unit of every sequence
+      for (int b0 = lane; b0 < B; b0 += 32) batch_tiles += unit_tiles(a, clamped_len(a, b0));
+      batch_tiles = __reduce_add_sync(0xffffffffu, batch_tiles);
+      const int layer_tiles = batch_tiles * per_batch, total = layer_tiles * a.nl;
+      p.run = max(kLeastRun, (total + (int)gridDim.x - 1) / (int)gridDim.x);
+      p.begin = (int)min((long long)total, (long long)blockIdx.x * p.run);
+      p.end = min(total, p.begin + p.run);
+      p.lz = p.begin < p.end ? p.begin / layer_tiles : 0;
+      const int rem = p.begin - p.lz * layer_tiles;
+      int passed = 0;
+      for (int b0 = 0; b0 < B && p.begin < p.end; b0 += 32) {
+        const int n = b0 + lane < B ? clamped_len(a, b0 + lane) : 0, v = unit_tiles(a, n) * per_batch;
+        int incl = v;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += x;
+        for (int o = 1; o < 32; o <<= 1) {
+          const int x = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += x;
+        }
+        const unsigned in = __ballot_sync(0xffffffffu, rem < passed + incl);
+        if (in) {
+          const int first = __ffs(in) - 1;  // the first sequence whose tiles end behind the place
+          p.b = b0 + first;
+          p.n = __shfl_sync(0xffffffffu, n, first);
+          p.tiles = unit_tiles(a, p.n);
+          passed += __shfl_sync(0xffffffffu, incl - v, first);
+          break;
+        }
+        passed += __shfl_sync(0xffffffffu, incl, 31);
       }
-      const unsigned in = __ballot_sync(0xffffffffu, rem < passed + incl);
-      if (in) {
-        const int first = __ffs(in) - 1;  // the first sequence whose tiles end behind the place
-        b = b0 + first;
-        tiles = __shfl_sync(0xffffffffu, v, first) / per_batch;
-        passed += __shfl_sync(0xffffffffu, incl - v, first);
-        break;
+      if (p.tiles) {
+        p.idx = (rem - passed) / p.tiles;
+        p.unit_at = p.lz * layer_tiles + passed + p.idx * p.tiles;
+        p.tile0 = p.begin - p.unit_at;
+      } else {
+        p.end = p.begin;
       }
-      passed += __shfl_sync(0xffffffffu, incl, 31);
     }
-    if (any) {
-      idx = (rem - passed) / tiles;
-      unit_at = lz * layer_tiles + passed + idx * tiles;
-      tile0 = begin - unit_at;
-    }
+    if (lane == 0) s_place = p;
   }
+  __syncthreads();
+  const int begin = s_place.begin, end_all = s_place.end, run = s_place.run, first_tiles = s_place.tiles;
+  if (a.cluster > 1 && begin == end_all)  // a piece without weight
+    for (int e = tid; e < R * (D + 4); e += kWarps * 32) s_part[e] = e % (D + 4) < 2 ? kNone : 0.0f;
 
   Tail tail = {0, 0, 0, 0, 0};
   for (int at = begin; at < end_all;) {
+    const int lz = s_place.lz, b = s_place.b, idx = s_place.idx, n = s_place.n;
+    const int tile0 = s_place.tile0, tiles = s_place.tiles, unit_at = s_place.unit_at;
     const int rt = idx % a.row_tiles;
     const int qi = SPARSE ? idx / a.row_tiles % a.nq : 0;  // the query token of a sparse unit
     const int h = idx / a.row_tiles / (SPARSE ? a.nq : 1);
     const long long u = ((long long)lz * B + b) * H + h;
-    const int n = clamped_len(a, b);
     const int tile1 = min(tiles, tile0 + (end_all - at));
     // row r of the unit is row `first + r step` of the [nl][B][hq][nq] rows
     const long long first = u * a.gq * a.nq + qi, step = SPARSE ? a.nq : 1;
@@ -520,25 +536,30 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm(D, NT)) cache8_attn_k
       tail.row0 = row0, tail.step = (int)step, tail.rows = my_rows;
       tail.pieces = (int)blockIdx.x - unit_at / run + 1;
     }
-    // the next unit
     at += tile1 - tile0;
-    unit_at += tiles;
-    tile0 = 0;
-    if (at < end_all && ++idx == per_batch) {
-      idx = 0;
-      do {
-        if (++b == B) b = 0, ++lz;
-        tiles = unit_tiles(a, b);
-      } while (tiles == 0);
+    if (tid == 0 && at < end_all) {  // the next unit
+      Place p = s_place;
+      p.unit_at += tiles;
+      p.tile0 = 0;
+      if (++p.idx == per_batch) {
+        p.idx = 0;
+        do {
+          if (++p.b == B) p.b = 0, ++p.lz;
+          p.n = p.lz < a.nl ? clamped_len(a, p.b) : 0;
+          p.tiles = unit_tiles(a, p.n);
+        } while (p.tiles == 0 && p.lz < a.nl);
+      }
+      s_place = p;
     }
-    __syncthreads();  // the outputs' memory takes tiles again
+    __syncthreads();  // the outputs' memory takes tiles again, and the next unit is in its place
+    if (s_place.tiles == 0) break;
   }
   if (a.cluster > 1) {
     namespace cgs = cooperative_groups;
     cgs::cluster_group cluster = cgs::this_cluster();
     cluster.sync();
-    if (tiles) {  // the rows in turn, a warp each
-      const int unit = blockIdx.x / a.cluster, rank = blockIdx.x % a.cluster;
+    if (first_tiles) {  // the rows in turn, a warp each
+      const int lz = s_place.lz, b = s_place.b, unit = blockIdx.x / a.cluster, rank = blockIdx.x % a.cluster;
       const int at = unit % per_batch, rt = at % a.row_tiles, qi = SPARSE ? at / a.row_tiles % a.nq : 0;
       const long long u = ((long long)lz * B + b) * H + at / a.row_tiles / (SPARSE ? a.nq : 1);
       const long long first = u * a.gq * a.nq + qi, step = SPARSE ? a.nq : 1;
@@ -569,7 +590,7 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm(D, NT)) cache8_attn_k
   // sequences that are empty: zeros
   const int seq_rows = a.hq * a.nq;
   for (long long e = blockIdx.x; e < (long long)a.nl * B; e += gridDim.x) {
-    if (unit_tiles(a, (int)(e % B))) continue;
+    if (clamped_len(a, (int)(e % B))) continue;
     float4* to = reinterpret_cast<float4*>(a.out + e * seq_rows * D);
     for (int i = tid; i < seq_rows * (D / 4); i += kWarps * 32) to[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   }

@@ -76,7 +76,7 @@ static_assert(kThreads == 256, "four histograms of 64 words of 16 bytes");
 // A thread has KPT consecutive keys in registers (keys.load gives them, of whatever stands behind
 // the last one), keys(i) gives key i (KPT 0: a run of them, read each time).
 template <int KPT, typename Keys>
-__device__ void pick_blocks(const Keys& keys, int nb, int k, int sink, int recent, int* out, PickShared& sh) {
+__device__ void pick_blocks(const Keys& keys, int nb, unsigned k, int sink, int recent, int* out, PickShared& sh) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int lo = sink, hi = nb - recent;
   uint32_t u[KPT ? KPT : 1];
@@ -110,7 +110,10 @@ __device__ void pick_blocks(const Keys& keys, int nb, int k, int sink, int recen
       const int high = shift;
       if (inside <= kFew) {
         each([&](uint32_t v) {
-          if (high == 32 || (v >> high) == (thr >> high)) sh.few[atomicAdd(&sh.n_few, 1u)] = v;
+          if (high == 32 || (v >> high) == (thr >> high)) {
+            const uint32_t at = atomicAdd(&sh.n_few, 1u);
+            if (at < kFew) sh.few[at] = v;  // (always, unless the values change meanwhile)
+          }
         });
         __syncthreads();
         const uint32_t mine = lane < inside ? sh.few[lane] : 0u;
@@ -182,11 +185,9 @@ __device__ void pick_blocks(const Keys& keys, int nb, int k, int sink, int recen
   sure = s_incl - sure, equal = e_incl - equal;
   for (int w = 0; w < warp; ++w) sure += sh.warp_sum[0][w], equal += sh.warp_sum[1][w];
   ordered([&](int i, int t) {
-    if (t == 1) out[sure++ + min(equal, need)] = i;
-    if (t == 2) {
-      if (equal < need) out[sure + equal] = i;
-      ++equal;
-    }
+    const uint32_t at = sure + min(equal, need);
+    if ((t == 1 || (t == 2 && equal < need)) && at < k) out[at] = i;  // (at < k unless the values change meanwhile)
+    sure += t == 1, equal += t == 2;
   });
 }
 template <typename Keys>
@@ -261,6 +262,7 @@ template <int D, bool FUSED, int CTAS>
 __global__ void __launch_bounds__(kThreads, CTAS) cache8_score_kernel(Cache8SelectArgs a, int chunks, int per, int nb_max) {
   constexpr int Q = D / 64;               // 16-byte pieces of a lane, of one bound of one block
   __shared__ PickShared sh;
+  __shared__ int s_n;
   extern __shared__ uint4 sq[];           // [tile][column][q8 <= 0, q8 >= 0][D / 16]
   const RowTiles rt = row_tiles(a.gq, a.nq);
   float* unit = reinterpret_cast<float*>(sq + rt.count * 8 * (D / 8));  // [tile][column] 2^e, negative: no row
@@ -273,6 +275,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) cache8_score_kernel(Cache8Sele
   const float* scales = a.scales + (((long long)(a.l0 + lz) * 2 * B + b) * H + h) * a.c.blocks();
   previous_kernel_done();
   const int n = max(0, min(a.lens[b], a.max_tokens));
+  if (threadIdx.x == 0) s_n = n;  // for the choice: its barriers depend on it, so one reading for all
   const int nb = (n + a.c.tb - 1) / a.c.tb;
   const int begin = chunk * per, end = min(nb, begin + per);
   if (!FUSED && begin >= nb) return;
@@ -370,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) cache8_score_kernel(Cache8Sele
     uint32_t* all = keys + a.nq * per;  // [nb] where a choice among more than kPickRegs needs them all
     const unsigned per_inv = 0xffffffffu / per + 1;  // i / per for i < 2^16, per > 1
     for (int i = chunk; i < a.nq; i += chunks) {
-      const int seen = seen_blocks(n, a.nq, i, a.c.tb);
+      const int seen = seen_blocks(s_n, a.nq, i, a.c.tb);
       int* out = a.sel + ((long long)u * a.nq + i) * a.n_select;
       if (seen <= a.n_select) {
         for (int j = threadIdx.x; j < a.n_select; j += kThreads) out[j] = j < seen ? j : -1;
@@ -401,9 +404,11 @@ __global__ void __launch_bounds__(kThreads) cache8_pick_kernel(Cache8SelectArgs 
   __shared__ PickShared sh;
   const long long row = blockIdx.x;  // [nl][B][H][nq]
   const int i = (int)(row % a.nq), b = (int)(row / a.nq / a.c.k.H % a.c.k.B);
+  __shared__ int s_n;
   previous_kernel_done();
-  const int n = max(0, min(a.lens[b], a.max_tokens));
-  const int nb = seen_blocks(n, a.nq, i, a.c.tb);
+  if (threadIdx.x == 0) s_n = max(0, min(a.lens[b], a.max_tokens));
+  __syncthreads();
+  const int nb = seen_blocks(s_n, a.nq, i, a.c.tb);
   int* out = a.sel + row * a.n_select;
   if (nb <= a.n_select) {
     for (int j = threadIdx.x; j < a.n_select; j += kThreads) out[j] = j < nb ? j : -1;
@@ -418,8 +423,11 @@ __global__ void __launch_bounds__(kThreads) cache8_pick_kernel(Cache8SelectArgs 
 // choice is made again by every CTA of the unit, which costs less than a second kernel or a wait;
 // the first one writes it down.
 // LISTED: the choice (more than kListed blocks stay) has been written by cache8_keep_kernel.
-__device__ void keep_blocks(const Cache8EvictArgs& a, int u, int n, int b, int lz, int h, bool write, int* list, PickShared& sh) {
-  const int tb = a.c.tb, nb = (n + tb - 1) / tb;
+__device__ void keep_blocks(const Cache8EvictArgs& a, int u, int b, int lz, int h, bool write, int* list, PickShared& sh) {
+  __shared__ int s_n;
+  if (threadIdx.x == 0) s_n = max(0, min(a.lens[b], a.c.k.T));
+  __syncthreads();  // one reading for all: barriers depend on it
+  const int n = s_n, tb = a.c.tb, nb = (n + tb - 1) / tb;
   const long long slice = ((long long)(a.l0 + lz) * a.c.k.B + b) * a.c.k.H + h;
   const float* mass = a.mass + slice * a.c.blocks();
   if (nb <= a.keep) {
@@ -435,7 +443,7 @@ __device__ void keep_blocks(const Cache8EvictArgs& a, int u, int n, int b, int l
   float* to_mass = a.to_mass + slice * a.to.blocks();
   const int m = min(nb, a.keep);
   if (lz == 0 && h == 0 && threadIdx.x == 0) a.to_lens[b] = nb > a.keep ? n - (nb - a.keep) * tb : n;
-  for (int j = threadIdx.x; j < a.to.blocks(); j += kThreads) to_mass[j] = j < m ? mass[list[j]] : 0.0f;
+  for (int j = threadIdx.x; j < a.to.blocks(); j += kThreads) to_mass[j] = j < m && (unsigned)list[j] < (unsigned)a.c.blocks() ? mass[list[j]] : 0.0f;
   if (kept != list)
     for (int j = threadIdx.x; j < a.keep; j += kThreads) kept[j] = list[j];
 }
@@ -445,7 +453,7 @@ __global__ void __launch_bounds__(kThreads) cache8_keep_kernel(Cache8EvictArgs a
   const unsigned H = a.c.k.H, B = a.c.k.B, u = blockIdx.x, bh = u / H;
   previous_kernel_done();
   const int b = bh % B;
-  keep_blocks(a, u, max(0, min(a.lens[b], a.c.k.T)), b, bh / B, u - bh * H, true, a.kept + (long long)u * a.keep, sh);
+  keep_blocks(a, u, b, bh / B, u - bh * H, true, a.kept + (long long)u * a.keep, sh);
 }
 
 template <bool LISTED>
@@ -458,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 4) cache8_evict_kernel(Cache8EvictAr
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, d = a.c.k.d;
   const int* kept = LISTED ? a.kept + (long long)u * a.keep : s_list;
   previous_kernel_done();
-  if (!LISTED) keep_blocks(a, u, max(0, min(a.lens[b], a.c.k.T)), b, lz, h, part == 0, s_list, sh);
+  if (!LISTED) keep_blocks(a, u, b, lz, h, part == 0, s_list, sh);
   const int shift = 31 - __clz(a.c.tb * d);  // bytes of a block: 2^10 .. 2^13
   const int pieces = (int)((((long long)a.keep << shift) + kPiece - 1) / kPiece);  // of the keys, and of the values
   for (int item = part * kWarps + warp; item < 2 * pieces; item += parts * kWarps) {
@@ -472,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 4) cache8_evict_kernel(Cache8EvictAr
 #pragma unroll
     for (int i = 0; i < kPiece / 512; ++i) {
       const int j = (int)((p0 + 512 * i) >> shift), blk = j < a.keep ? kept[j] : -1;
-      there[i] = blk >= 0;
+      there[i] = (unsigned)blk < (unsigned)a.c.blocks();
       if (there[i]) v[i] = __ldcs(reinterpret_cast<const uint4*>(src + ((long long)blk << shift) + ((p0 + 512 * i) & ((1 << shift) - 1))));
     }
 #pragma unroll
@@ -483,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, 4) cache8_evict_kernel(Cache8EvictAr
     const int last = (int)(((long long)piece * kPiece + kPiece - 1) >> shift);
     for (int j = (int)((((long long)piece * kPiece - 1) >> shift) + 1); j <= last && j < a.keep; ++j) {
       const int blk = kept[j];
-      if (blk < 0) break;
+      if ((unsigned)blk >= (unsigned)a.c.blocks()) break;
       if (lane == 31) a.to_scales[slice * a.to.blocks() + j] = a.scales[slice * a.c.blocks() + blk];
       if (s == 0 && a.bounds && lane < d / 8)
         reinterpret_cast<uint4*>(a.to_bounds)[(unit * a.to.blocks() + j) * (d / 8) + lane] =

@@ -116,6 +116,21 @@ def test_append_extremes(code):
     c.same()
 
 
+@pytest.mark.parametrize("code", [cg.CACHE8_INT8, cg.CACHE8_E4M3])
+def test_append_again_after_draft_tokens_are_dropped(code):
+    """Positions go back into a block, to its start and into the block before, and are stored again."""
+    need_gpu()
+    L, B, H, T, d, tb = 1, 4, 2, 128, 64, 32
+    c = Cache(L, B, H, T, d, code, tb)
+    gen = torch.Generator().manual_seed(8)
+    c.append(_new(gen, L, 2, B, H, 70, d), [0] * B)
+    c.append(_new(gen, L, 2, B, H, 5, d, gain=8), [69, 64, 60, 33])
+    c.append(_new(gen, L, 2, B, H, 5, d, gain=0.25), [66, 64, 32, 34])
+    c.same()
+    q = _new(gen, L, B, 3 * H, 1, d)
+    _check_attention(c, q, [71, 69, 37, 39])
+
+
 def test_append_off_the_cache_stores_nothing_there():
     need_gpu()
     L, B, H, T, d, tb = 1, 6, 2, 64, 64, 32
