@@ -375,6 +375,7 @@ def alloc_cache8(kvd, c8, device="cuda"):
 
 
 # These calls are made once a layer and token: what their checks cost is a large part of a short call.
+_BF16, _F32, _I32, _U8, _I8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8, torch.int8
 
 
 def _cache8_counts(kvd, c8):
@@ -433,10 +434,10 @@ def cg_cache8_append(kvd, c8, layer0, new, pos, counts, codes, scales, bounds, s
         return
     dev = _device_of(codes, "codes")
     status = lib().cg_cache8_append(
-        kvd, c8, layer0, shape[0], shape[4], _at(new, torch.bfloat16, "new", 1, dev),
-        _at(pos, torch.int32, "pos", B, dev), _at(counts, torch.int32, "counts", B, dev),
-        _at(codes, torch.uint8, "codes", cb, dev), _at(scales, torch.float32, "scales", sc, dev),
-        _at(bounds, torch.int8, "bounds", bb, dev), _here(stream, dev))
+        kvd, c8, layer0, shape[0], shape[4], _at(new, _BF16, "new", 1, dev),
+        _at(pos, _I32, "pos", B, dev), _at(counts, _I32, "counts", B, dev),
+        _at(codes, _U8, "codes", cb, dev), _at(scales, _F32, "scales", sc, dev),
+        _at(bounds, _I8, "bounds", bb, dev), _here(stream, dev))
     _check(status, "cg_cache8_append")
 
 
@@ -457,11 +458,11 @@ def cg_cache8_attention(kvd, c8, at, q, codes, scales, lens, out, workspace, sel
     rows = at.n_layers * B * at.q_tokens
     nq = rows * at.q_heads * kvd.d_head
     status = lib().cg_cache8_attention(
-        kvd, c8, at, _at(q, torch.bfloat16, "q", nq, dev),
-        _at(codes, torch.uint8, "codes", cb, dev), _at(scales, torch.float32, "scales", sc, dev),
-        _at(lens, torch.int32, "lens", B, dev), _at(sel, torch.int32, "sel", rows * kvd.heads * at.n_select, dev),
-        _at(out, torch.float32, "out", nq, dev), _at(mass, torch.float32, "mass", mc, dev),
-        _at(workspace, torch.uint8, "workspace", 1, dev), workspace.numel(), _here(stream, dev))
+        kvd, c8, at, _at(q, _BF16, "q", nq, dev),
+        _at(codes, _U8, "codes", cb, dev), _at(scales, _F32, "scales", sc, dev),
+        _at(lens, _I32, "lens", B, dev), _at(sel, _I32, "sel", rows * kvd.heads * at.n_select, dev),
+        _at(out, _F32, "out", nq, dev), _at(mass, _F32, "mass", mc, dev),
+        _at(workspace, _U8, "workspace", 1, dev), workspace.numel(), _here(stream, dev))
     _check(status, "cg_cache8_attention")
     return out
 
@@ -481,9 +482,9 @@ def cg_cache8_select(kvd, c8, sd, q, scales, bounds, lens, sel, workspace, strea
     rows = sd.n_layers * B * sd.q_tokens
     status = lib().cg_cache8_select(
         kvd, c8, sd,
-        _at(q, torch.bfloat16, "q", rows * sd.q_heads * kvd.d_head, dev), _at(scales, torch.float32, "scales", sc, dev),
-        _at(bounds, torch.int8, "bounds", bb, dev), _at(lens, torch.int32, "lens", B, dev),
-        _at(sel, torch.int32, "sel", rows * kvd.heads * sd.n_select, dev), _at(workspace, torch.uint8, "workspace", 1, dev),
+        _at(q, _BF16, "q", rows * sd.q_heads * kvd.d_head, dev), _at(scales, _F32, "scales", sc, dev),
+        _at(bounds, _I8, "bounds", bb, dev), _at(lens, _I32, "lens", B, dev),
+        _at(sel, _I32, "sel", rows * kvd.heads * sd.n_select, dev), _at(workspace, _U8, "workspace", 1, dev),
         workspace.numel(), _here(stream, dev))
     _check(status, "cg_cache8_select")
     return sel
@@ -497,13 +498,13 @@ def cg_cache8_evict(kvd, c8, ev, lens, codes, scales, bounds, mass, to_kvd, to_c
     tcb, tsc, tbb, tmc = _cache8_counts(to_kvd, c8)
     B, dev = kvd.batch, _device_of(codes, "codes")
     status = lib().cg_cache8_evict(
-        kvd, c8, ev, _at(lens, torch.int32, "lens", B, dev),
-        _at(codes, torch.uint8, "codes", cb, dev), _at(scales, torch.float32, "scales", sc, dev),
-        _at(bounds, torch.int8, "bounds", bb, dev), _at(mass, torch.float32, "mass", mc, dev), to_kvd,
-        _at(to_codes, torch.uint8, "to_codes", tcb, dev), _at(to_scales, torch.float32, "to_scales", tsc, dev),
-        _at(to_bounds, torch.int8, "to_bounds", tbb, dev), _at(to_mass, torch.float32, "to_mass", tmc, dev),
-        _at(to_lens, torch.int32, "to_lens", B, dev),
-        _at(kept, torch.int32, "kept", ev.n_layers * B * kvd.heads * ev.keep_blocks, dev), _here(stream, dev))
+        kvd, c8, ev, _at(lens, _I32, "lens", B, dev),
+        _at(codes, _U8, "codes", cb, dev), _at(scales, _F32, "scales", sc, dev),
+        _at(bounds, _I8, "bounds", bb, dev), _at(mass, _F32, "mass", mc, dev), to_kvd,
+        _at(to_codes, _U8, "to_codes", tcb, dev), _at(to_scales, _F32, "to_scales", tsc, dev),
+        _at(to_bounds, _I8, "to_bounds", tbb, dev), _at(to_mass, _F32, "to_mass", tmc, dev),
+        _at(to_lens, _I32, "to_lens", B, dev),
+        _at(kept, _I32, "kept", ev.n_layers * B * kvd.heads * ev.keep_blocks, dev), _here(stream, dev))
     _check(status, "cg_cache8_evict")
 
 

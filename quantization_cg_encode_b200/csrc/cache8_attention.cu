@@ -335,151 +335,151 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm(D, NT)) cache8_attn_k
 
     for (int i0 = 0; i0 < n_mine; i0 += kStages) {
 #pragma unroll
-     for (int st = 0; st < kStages; ++st) {
-      const int i = i0 + st;
-      if (i >= n_mine) break;
-      const int t0 = starts[st], ahead = (st + kStages - 1) % kStages;
-      fetch(i + kStages - 1, starts[ahead], ahead);
-      starts[st] = first_token(i + kStages, blk_ahead);
-      if (SPARSE) blk_ahead = listed(i + kStages + 1);
-      copies_wait<kStages - 1>();
-      __syncwarp();
-      if (SPARSE && t0 < 0) continue;  // warp-uniform
-      uint32_t pieces[CH / 2];  // pieces 2 jj, 2 jj + 1 of this lane's ldmatrix row
+      for (int st = 0; st < kStages; ++st) {
+        const int i = i0 + st;
+        if (i >= n_mine) break;
+        const int t0 = starts[st], ahead = (st + kStages - 1) % kStages;
+        fetch(i + kStages - 1, starts[ahead], ahead);
+        starts[st] = first_token(i + kStages, blk_ahead);
+        if (SPARSE) blk_ahead = listed(i + kStages + 1);
+        copies_wait<kStages - 1>();
+        __syncwarp();
+        if (SPARSE && t0 < 0) continue;  // warp-uniform
+        uint32_t pieces[CH / 2];  // pieces 2 jj, 2 jj + 1 of this lane's ldmatrix row
 #pragma unroll
-      for (int jj = 0; jj < CH / 2; ++jj) pieces[jj] = ring + st * (2 * TILE) + matrix_piece[jj];
-      const float kscale = s_scale[warp][st][0];
-      const float vexp = (float)((int)(__float_as_uint(s_scale[warp][st][1]) >> 23) - 127);
+        for (int jj = 0; jj < CH / 2; ++jj) pieces[jj] = ring + st * (2 * TILE) + matrix_piece[jj];
+        const float kscale = s_scale[warp][st][0];
+        const float vexp = (float)((int)(__float_as_uint(s_scale[warp][st][1]) >> 23) - 127);
 
-      // scores of 16 tokens x R rows
-      float s[NT][4];
+        // scores of 16 tokens x R rows
+        float s[NT][4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.0f;
+        for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.0f;
 #pragma unroll
-      for (int jj = 0; jj < CH / 2; ++jj) {
-        uint32_t w[4];  // token g, g + 8 of piece 2 jj, then of the next
-        ldmatrix_x4(w, pieces[jj]);
+        for (int jj = 0; jj < CH / 2; ++jj) {
+          uint32_t w[4];  // token g, g + 8 of piece 2 jj, then of the next
+          ldmatrix_x4(w, pieces[jj]);
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          uint32_t af[4];
-          codes_to_f16<CODE>(w[2 * k], af[0], af[2]);
-          codes_to_f16<CODE>(w[2 * k + 1], af[1], af[3]);
+          for (int k = 0; k < 2; ++k) {
+            uint32_t af[4];
+            codes_to_f16<CODE>(w[2 * k], af[0], af[2]);
+            codes_to_f16<CODE>(w[2 * k + 1], af[1], af[3]);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma_f16_16816(s[nt], af, bq[nt][2 * jj + k][0], bq[nt][2 * jj + k][1]);
-        }
-      }
-      // s[nt][0..3]: token g (0, 1) or g + 8 (2, 3), row 2c + (index & 1); x = factor s
-      float factor[NT][2], x[NT][4];  // x - M
-      bool over = false;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          factor[nt][j] = fmaxf(kscale * qs[nt][j], 1.0e-37f);  // (0 times -inf is no -inf)
-          if (t0 + 16 > all_see) {
-            const int t = t0 + g, see = min(lim[nt][j], end);
-            s[nt][j] = t < see ? s[nt][j] : -INFINITY;
-            s[nt][j + 2] = t + 8 < see ? s[nt][j + 2] : -INFINITY;
+            for (int nt = 0; nt < NT; ++nt) mma_f16_16816(s[nt], af, bq[nt][2 * jj + k][0], bq[nt][2 * jj + k][1]);
           }
-          x[nt][j] = __fmaf_rn(s[nt][j], factor[nt][j], -m_run[nt][j]);
-          x[nt][j + 2] = __fmaf_rn(s[nt][j + 2], factor[nt][j], -m_run[nt][j]);
-          over |= (!PAIR || c < 2) && fmaxf(x[nt][j], x[nt][j + 2]) > fminf(kLag, mv_m[nt][j] + (kLag - vexp));
         }
-      if (__any_sync(0xffffffffu, over)) {
+        // s[nt][0..3]: token g (0, 1) or g + 8 (2, 3), row 2c + (index & 1); x = factor s
+        float factor[NT][2], x[NT][4];  // x - M
+        bool over = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const float top = column_max(fmaxf(s[nt][j], s[nt][j + 2])) * factor[nt][j];
-            const float m_old = m_run[nt][j], mv_old = mv_run[nt][j];
-            const float m = fmaxf(m_old, top), mv = fmaxf(mv_old, top + vexp);
-            float fv = ex2(mv_old - mv);
-            if (PAIR) {  // columns 4-7 go with 0-3
-              const float other = __shfl_xor_sync(0xffffffffu, fv, 2);
-              fv = c < 2 ? fv : other;
+            factor[nt][j] = fmaxf(kscale * qs[nt][j], 1.0e-37f);  // (0 times -inf is no -inf)
+            if (t0 + 16 > all_see) {
+              const int t = t0 + g, see = min(lim[nt][j], end);
+              s[nt][j] = t < see ? s[nt][j] : -INFINITY;
+              s[nt][j + 2] = t + 8 < see ? s[nt][j + 2] : -INFINITY;
             }
-            m_run[nt][j] = m, mv_run[nt][j] = mv, mv_m[nt][j] = mv - m;
-            l_run[nt][j] *= ex2(m_old - m);
-            x[nt][j] = __fmaf_rn(s[nt][j], factor[nt][j], -m);
-            x[nt][j + 2] = __fmaf_rn(s[nt][j + 2], factor[nt][j], -m);
-#pragma unroll
-            for (int k = 0; k < CH; ++k) o[nt][k][j] *= fv, o[nt][k][j + 2] *= fv;
+            x[nt][j] = __fmaf_rn(s[nt][j], factor[nt][j], -m_run[nt][j]);
+            x[nt][j + 2] = __fmaf_rn(s[nt][j + 2], factor[nt][j], -m_run[nt][j]);
+            over |= (!PAIR || c < 2) && fmaxf(x[nt][j], x[nt][j + 2]) > fminf(kLag, mv_m[nt][j] + (kLag - vexp));
           }
-      }
-      uint32_t bhi[NT][2], blo[NT][2];
-      float tile_sum[2 * NT];  // of this lane's two tokens: column (nt, j)
+        if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float pv[4];
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const float p0 = ex2(x[nt][j]), p1 = ex2(x[nt][j + 2]);
-          tile_sum[2 * nt + j] = p0 + p1;
-          l_run[nt][j] += tile_sum[2 * nt + j];
-          // p s_V relative to M': p 2^f <= 2^(kLag + kShift), so a factor of over 2^100 meets a p below 2^-85, whose
-          // row's sum holds a weight of 1 at least: nothing that a result in fp32 could show
-          const float f = ex2(fminf((vexp + kShift) - mv_m[nt][j], 100.0f));
-          pv[j] = p0 * f, pv[j + 2] = p1 * f;
+            for (int j = 0; j < 2; ++j) {
+              const float top = column_max(fmaxf(s[nt][j], s[nt][j + 2])) * factor[nt][j];
+              const float m_old = m_run[nt][j], mv_old = mv_run[nt][j];
+              const float m = fmaxf(m_old, top), mv = fmaxf(mv_old, top + vexp);
+              float fv = ex2(mv_old - mv);
+              if (PAIR) {  // columns 4-7 go with 0-3
+                const float other = __shfl_xor_sync(0xffffffffu, fv, 2);
+                fv = c < 2 ? fv : other;
+              }
+              m_run[nt][j] = m, mv_run[nt][j] = mv, mv_m[nt][j] = mv - m;
+              l_run[nt][j] *= ex2(m_old - m);
+              x[nt][j] = __fmaf_rn(s[nt][j], factor[nt][j], -m);
+              x[nt][j + 2] = __fmaf_rn(s[nt][j + 2], factor[nt][j], -m);
+#pragma unroll
+              for (int k = 0; k < CH; ++k) o[nt][k][j] *= fv, o[nt][k][j + 2] *= fv;
+            }
         }
+        uint32_t bhi[NT][2], blo[NT][2];
+        float tile_sum[2 * NT];  // of this lane's two tokens: column (nt, j)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const __half2 hi = __floats2half2_rn(pv[2 * j], pv[2 * j + 1]);
-          const float2 back = __half22float2(hi);
-          const __half2 lo = __floats2half2_rn(pv[2 * j] - back.x, pv[2 * j + 1] - back.y);
-          if (PAIR) {
-            const uint32_t other = __shfl_xor_sync(0xffffffffu, *reinterpret_cast<const uint32_t*>(&lo), 2);
-            bhi[nt][j] = transpose_8x8(c < 2 ? *reinterpret_cast<const uint32_t*>(&hi) : other);
-          } else {
-            bhi[nt][j] = transpose_8x8(*reinterpret_cast<const uint32_t*>(&hi));
-            blo[nt][j] = transpose_8x8(*reinterpret_cast<const uint32_t*>(&lo));
+        for (int nt = 0; nt < NT; ++nt) {
+          float pv[4];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float p0 = ex2(x[nt][j]), p1 = ex2(x[nt][j + 2]);
+            tile_sum[2 * nt + j] = p0 + p1;
+            l_run[nt][j] += tile_sum[2 * nt + j];
+            // p s_V relative to M': p 2^f <= 2^(kLag + kShift), so a factor of over 2^100 meets a p below 2^-85, whose
+            // row's sum holds a weight of 1 at least: nothing that a result in fp32 could show
+            const float f = ex2(fminf((vexp + kShift) - mv_m[nt][j], 100.0f));
+            pv[j] = p0 * f, pv[j + 2] = p1 * f;
           }
-        }
-      }
-      if (MASS) {
-        // over the eight lanes of a column, each step halving the columns that a lane keeps: lane g
-        // ends with one
-        float ref[2 * NT];
 #pragma unroll
-        for (int k = 0; k < 2 * NT; ++k) ref[k] = m_run[k >> 1][k & 1];
-        int o = 4;
-#pragma unroll
-        for (int half = NT; half >= 1; half >>= 1, o <<= 1) {
-          const bool up = lane & o;
-#pragma unroll
-          for (int k = 0; k < half; ++k) {
-            const float keep = up ? tile_sum[half + k] : tile_sum[k], give = up ? tile_sum[k] : tile_sum[half + k];
-            tile_sum[k] = keep + __shfl_xor_sync(0xffffffffu, give, o);
-            ref[k] = up ? ref[half + k] : ref[k];
-          }
-        }
-#pragma unroll
-        for (; o <= 16; o <<= 1) tile_sum[0] += __shfl_xor_sync(0xffffffffu, tile_sum[0], o);
-        // the column that the halving left: its high bit was decided first
-        const int col = NT == 2 ? (g & 1) * 2 + (g >> 1 & 1) : g & 1;
-        const int r = rt * R + (col >> 1) * 8 + 2 * c + (col & 1);
-        if (g < 2 * NT && r < rows)
-          a.tile_mass[(first + r) * ((a.max_tokens + 15) >> 4) + (tile0 + warp + i * kWarps)] = make_float2(tile_sum[0], ref[0]);
-      }
-      // o[channel][row] += codes^T p
-#pragma unroll
-      for (int jj = 0; jj < CH / 2; ++jj) {
-        uint32_t w[4];  // tokens 2c, 2c + 1, then 2c + 8, 2c + 9, of channels 2g, 2g + 1 of piece 2 jj; of the next
-        ldmatrix_x4_trans(w, pieces[jj] + TILE);
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          uint32_t af[4];
-          if (CODE == kCache8E4m3) w[2 * k] = __byte_perm(w[2 * k], 0, 0x3120), w[2 * k + 1] = __byte_perm(w[2 * k + 1], 0, 0x3120);
-          codes_to_f16<CODE>(w[2 * k], af[0], af[1]);
-          codes_to_f16<CODE>(w[2 * k + 1], af[2], af[3]);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            mma_f16_16816(o[nt][2 * jj + k], af, bhi[nt][0], bhi[nt][1]);
-            if (!PAIR) mma_f16_16816(o[nt][2 * jj + k], af, blo[nt][0], blo[nt][1]);
+          for (int j = 0; j < 2; ++j) {
+            const __half2 hi = __floats2half2_rn(pv[2 * j], pv[2 * j + 1]);
+            const float2 back = __half22float2(hi);
+            const __half2 lo = __floats2half2_rn(pv[2 * j] - back.x, pv[2 * j + 1] - back.y);
+            if (PAIR) {
+              const uint32_t other = __shfl_xor_sync(0xffffffffu, *reinterpret_cast<const uint32_t*>(&lo), 2);
+              bhi[nt][j] = transpose_8x8(c < 2 ? *reinterpret_cast<const uint32_t*>(&hi) : other);
+            } else {
+              bhi[nt][j] = transpose_8x8(*reinterpret_cast<const uint32_t*>(&hi));
+              blo[nt][j] = transpose_8x8(*reinterpret_cast<const uint32_t*>(&lo));
+            }
           }
         }
+        if (MASS) {
+          // over the eight lanes of a column, each step halving the columns that a lane keeps: lane g
+          // ends with one
+          float ref[2 * NT];
+#pragma unroll
+          for (int k = 0; k < 2 * NT; ++k) ref[k] = m_run[k >> 1][k & 1];
+          int o = 4;
+#pragma unroll
+          for (int half = NT; half >= 1; half >>= 1, o <<= 1) {
+            const bool up = lane & o;
+#pragma unroll
+            for (int k = 0; k < half; ++k) {
+              const float keep = up ? tile_sum[half + k] : tile_sum[k], give = up ? tile_sum[k] : tile_sum[half + k];
+              tile_sum[k] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+              ref[k] = up ? ref[half + k] : ref[k];
+            }
+          }
+#pragma unroll
+          for (; o <= 16; o <<= 1) tile_sum[0] += __shfl_xor_sync(0xffffffffu, tile_sum[0], o);
+          // the column that the halving left: its high bit was decided first
+          const int col = NT == 2 ? (g & 1) * 2 + (g >> 1 & 1) : g & 1;
+          const int r = rt * R + (col >> 1) * 8 + 2 * c + (col & 1);
+          if (g < 2 * NT && r < rows)
+            a.tile_mass[(first + r) * ((a.max_tokens + 15) >> 4) + (tile0 + warp + i * kWarps)] = make_float2(tile_sum[0], ref[0]);
+        }
+        // o[channel][row] += codes^T p
+#pragma unroll
+        for (int jj = 0; jj < CH / 2; ++jj) {
+          uint32_t w[4];  // tokens 2c, 2c + 1, then 2c + 8, 2c + 9, of channels 2g, 2g + 1 of piece 2 jj; of the next
+          ldmatrix_x4_trans(w, pieces[jj] + TILE);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            uint32_t af[4];
+            if (CODE == kCache8E4m3) w[2 * k] = __byte_perm(w[2 * k], 0, 0x3120), w[2 * k + 1] = __byte_perm(w[2 * k + 1], 0, 0x3120);
+            codes_to_f16<CODE>(w[2 * k], af[0], af[1]);
+            codes_to_f16<CODE>(w[2 * k + 1], af[2], af[3]);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              mma_f16_16816(o[nt][2 * jj + k], af, bhi[nt][0], bhi[nt][1]);
+              if (!PAIR) mma_f16_16816(o[nt][2 * jj + k], af, blo[nt][0], blo[nt][1]);
+            }
+          }
+        }
+        __syncwarp();  // the stage is free for the next fetch
       }
-      __syncwarp();  // the stage is free for the next fetch
-     }
     }
 
     // merge the warps: o relative to the CTA's maxima
