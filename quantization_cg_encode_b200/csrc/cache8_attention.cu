@@ -50,8 +50,15 @@ constexpr int ctas_per_sm(int d, int nt) { return d == 128 && nt == 2 ? 1 : 2; }
 constexpr int kStages = 3;
 constexpr int kSms = 148;               // what the number of CTAs is sized for
 constexpr int kLeastRun = 8;            // tiles of a run at least
+constexpr int kCombineWarps = 8;
+constexpr int kFewPieces = 4;            // of a unit: read one after another
 constexpr int kMaxCluster = 8;
 constexpr int kClusterTiles = 16;       // tiles of a warp in a unit that a cluster takes
+// Clusters of a size that the GPU holds at once, at one or two CTAs an SM: its parts' numbers of SMs are no
+// multiples of 4 or 8.  (16 units on 8 CTAs each, one an SM, took two turns: 17.2 us, on 4 each 10.2.)
+constexpr long long clusters_at_once(int size, int per_sm) {
+  return size == 8 ? (per_sm == 2 ? 33 : 15) : size == 4 ? (per_sm == 2 ? 71 : 33) : kSms / size * per_sm;
+}
 constexpr float kNone = -1.0e30f;       // a running maximum that has seen nothing
 constexpr float kLag = 8.0f;            // how far a value may lie above the running maximum
 constexpr float kShift = 7.0f;          // 2^kShift p' <= 2^15 fits fp16
@@ -622,6 +629,69 @@ __global__ void __launch_bounds__(D) cache8_combine_kernel(Cache8AttnArgs a, boo
   if (mass && ch == 0) a.stats[row] = make_float2(m, l > 0.0f ? 1.0f / l : 0.0f);
 }
 
+// The same where a unit may be cut into as many pieces as there are CTAs: they are read side by side, first all
+// maxima and sums, a piece a thread, then the outputs, which the warps take in turn.  (One head of 32768
+// tokens, 256 pieces: 16 us in all, 57 with the kernel above.)
+template <int D>
+__global__ void __launch_bounds__(kCombineWarps * 32) cache8_combine_many_kernel(Cache8AttnArgs a, bool mass) {
+  constexpr int N = D / 32;
+  __shared__ float s_stat[kCombineWarps][3], s_o[kCombineWarps][D];
+  const int R = 8 * a.nt, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = blockIdx.y;
+  previous_kernel_done();
+  dependents_may_launch();
+  const Tail tail = reinterpret_cast<const Tail*>(a.tails)[blockIdx.x];
+  if (r >= tail.rows || tail.pieces == 0) return;
+  auto piece = [&](int i) {  // 0: the last
+    return a.part + ((long long)(blockIdx.x - i) * 2 + (i ? 1 : 0)) * R * (D + 4) + r * (D + 4);
+  };
+  // a thread's pieces, then a warp's, then all: m, m' and the sum relative to m
+  float m = kNone, mv = kNone, l = 0.0f;
+  for (int i = tid; i < tail.pieces; i += kCombineWarps * 32) {
+    const float4 st = *reinterpret_cast<const float4*>(piece(i));
+    const float m2 = fmaxf(m, st.x);
+    l = l * ex2(m - m2) + st.z * ex2(st.x - m2);
+    m = m2, mv = fmaxf(mv, st.y);
+  }
+  const float m_warp = warp_max_f32(m), mv_warp = warp_max_f32(mv);
+  l *= ex2(m - m_warp);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  if (lane == 0) s_stat[warp][0] = m_warp, s_stat[warp][1] = mv_warp, s_stat[warp][2] = l;
+  __syncthreads();
+  m = mv = kNone, l = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kCombineWarps; ++w) m = fmaxf(m, s_stat[w][0]), mv = fmaxf(mv, s_stat[w][1]);
+#pragma unroll
+  for (int w = 0; w < kCombineWarps; ++w) l = __fmaf_rn(s_stat[w][2], ex2(s_stat[w][0] - m), l);
+  float acc[N];
+#pragma unroll
+  for (int j = 0; j < N; ++j) acc[j] = 0.0f;
+#pragma unroll 8
+  for (int i = warp; i < tail.pieces; i += kCombineWarps) {
+    const float* v = piece(i);
+    const float f = ex2(v[1] - mv);
+    if constexpr (N == 4) {
+      const float4 o = *reinterpret_cast<const float4*>(v + 4 + 4 * lane);
+      acc[0] = __fmaf_rn(o.x, f, acc[0]), acc[1] = __fmaf_rn(o.y, f, acc[1]), acc[2] = __fmaf_rn(o.z, f, acc[2]), acc[3] = __fmaf_rn(o.w, f, acc[3]);
+    } else {
+      const float2 o = *reinterpret_cast<const float2*>(v + 4 + 2 * lane);
+      acc[0] = __fmaf_rn(o.x, f, acc[0]), acc[1] = __fmaf_rn(o.y, f, acc[1]);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < N; ++j) s_o[warp][N * lane + j] = acc[j];
+  __syncthreads();
+  const long long row = tail.row0 + (long long)r * tail.step;
+  const float f = l > 0.0f ? ex2(mv - m - kShift) / l : 0.0f;
+  for (int ch = tid; ch < D; ch += kCombineWarps * 32) {
+    float sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kCombineWarps; ++w) sum += s_o[w][ch];
+    a.out[row * D + ch] = sum * f;
+  }
+  if (mass && tid == 0) a.stats[row] = make_float2(m, l > 0.0f ? 1.0f / l : 0.0f);
+}
+
 // mass[block] (+)= sum over the unit's rows and the block's tiles of p: 32 blocks a CTA, its warps
 // take rows in turn
 __global__ void __launch_bounds__(256) cache8_mass_kernel(Cache8AttnArgs a, int chunks) {
@@ -699,7 +769,7 @@ void plan(Cache8AttnArgs& a) {
   // the second kernel 24.3 (33.5, 50.9).
   const long long unit = a.n_select ? (long long)a.n_select * (a.c.tb / 16) : (a.max_tokens + 15) / 16;
   int size = 1;
-  while (size < kMaxCluster && size * kWarps < unit && units(a) * size * 2 <= most) size *= 2;
+  while (size < kMaxCluster && size * kWarps < unit && units(a) <= clusters_at_once(2 * size, ctas_per_sm(a.c.k.d, a.nt))) size *= 2;
   const bool even = (a.c.k.B == 1 || a.n_select) && 4 * units(a) * size >= 3 * most;
   a.cluster = units(a) <= most && (even || unit <= (long long)size * kWarps * kClusterTiles) ? size : 0;
   if (a.cluster) a.ctas = (int)units(a) * size;
@@ -747,7 +817,11 @@ template <int D>
 cudaError_t launch_d(const Cache8AttnArgs& a, cudaStream_t st) {
   const cudaError_t e = a.c.code == kCache8Int8 ? launch_rows<D, kCache8Int8>(a, st) : launch_rows<D, kCache8E4m3>(a, st);
   if (e != cudaSuccess || a.cluster) return e;
-  return launch_after(cache8_combine_kernel<D>, dim3(a.ctas, 8 * a.nt), D, 0, st, 1, a, a.mass != nullptr);
+  const int rows = a.n_select ? a.gq : a.gq * a.nq;
+  const dim3 grid(a.ctas, rows < 8 * a.nt ? rows : 8 * a.nt);
+  // pieces of a unit, were all of one length
+  if (a.ctas <= kFewPieces * units(a)) return launch_after(cache8_combine_kernel<D>, grid, D, 0, st, 1, a, a.mass != nullptr);
+  return launch_after(cache8_combine_many_kernel<D>, grid, kCombineWarps * 32, 0, st, 1, a, a.mass != nullptr);
 }
 
 int mass_chunks(const Cache8AttnArgs& a) { return (a.c.blocks() + 31) / 32; }

@@ -210,6 +210,31 @@ def test_attention_of_long_sequences(code, B, T, gq, nq):
     _check_attention(c, q, lens, max_tokens=T - 1)
 
 
+@pytest.mark.parametrize("d,T,gq,nq", [(128, 40960, 4, 1), (64, 33024, 2, 3), (128, 20480, 8, 2)])
+def test_attention_of_one_long_head_cut_into_many_pieces_with_block_weights(d, T, gq, nq):
+    """One unit, of which every CTA has a piece: up to 296 of them, merged side by side."""
+    need_gpu()
+    tb, lens = 64, [T - 5]
+    c = _filled(1, 1, 1, T, d, cg.CACHE8_INT8, tb, lens, seed=T, spread=20)
+    q = _new(torch.Generator().manual_seed(gq), 1, 1, gq, nq, d, gain=2.0)
+    ref, want, spread, big = _check_attention(c, q, lens)
+    eps = big.max() * (d / 16 + 4) * 2.0 ** -23 + 40 * 2.0 ** -22
+    mass = torch.full((1, 1, 1, T // tb), 7.0, dtype=torch.float32, device="cuda")
+    got = _attend(c, q, lens, mass=mass)
+    _close(got, ref, spread, big, d)
+    assert np.all(np.abs(mass.cpu().numpy().astype(np.float64) - want) <= 2 * eps * want)
+
+
+@pytest.mark.parametrize("B,gq,nq", [(4, 8, 2), (8, 4, 1), (17, 3, 1)])
+def test_attention_of_units_around_the_number_of_clusters_at_once(B, gq, nq):
+    need_gpu()
+    T, H, d = 1024, 4, 128
+    lens = [T - 60 * b for b in range(B)]
+    c = _filled(1, B, H, T, d, cg.CACHE8_E4M3, 32, lens, seed=B)
+    q = _new(torch.Generator().manual_seed(B), 1, B, H * gq, nq, d, gain=1.5)
+    _check_attention(c, q, lens)
+
+
 @pytest.mark.parametrize("d,gq,nq", [(128, 2, 1), (64, 3, 4)])
 def test_attention_runs_over_many_ragged_sequences_with_block_weights(d, gq, nq):
     """More units than CTAs: a CTA's run holds whole sequences and pieces of two more."""
