@@ -20,7 +20,8 @@
 // The value scale is a power of two, 2^v: p s_V = 2^(x + v) is kept relative to its own running
 // maximum M', so that no ratio of scales costs fp16 range, and the sum of p relative to M:
 //   out = (sum 2^(x + v - M') code) / (sum 2^(x - M)) 2^(M' - M).
-// M and M' follow the maxima lazily (they move when a value is 2^8 above).
+// M and M' are whole numbers, so that M' - M is exact; they follow the maxima lazily (they move when
+// a value is 2^8 above).
 //
 // All tiles of the call (every unit's, a unit being the query rows of one layer, sequence and KV
 // head, 8 or 16 of them) stand in one row, of which every CTA takes an equal run, so that ragged
@@ -60,6 +61,7 @@ constexpr long long clusters_at_once(int size, int per_sm) {
   return size == 8 ? (per_sm == 2 ? 33 : 15) : size == 4 ? (per_sm == 2 ? 71 : 33) : kSms / size * per_sm;
 }
 constexpr float kNone = -1.0e30f;       // a running maximum that has seen nothing
+constexpr float kDeep = -80.0f;         // the least power of two that a result is multiplied with at once
 constexpr float kLag = 8.0f;            // how far a value may lie above the running maximum
 constexpr float kShift = 7.0f;          // 2^kShift p' <= 2^15 fits fp16
 
@@ -72,6 +74,10 @@ __device__ __forceinline__ float ex2(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
+}
+// 2^e / l (0 where l is) in two factors: a result that fp32 holds may need a power of two that it does not
+__device__ __forceinline__ float2 last_factor(float e, float l) {
+  return make_float2(l > 0.0f ? ex2(fmaxf(e, kDeep)) / l : 0.0f, ex2(fminf(e - kDeep, 0.0f)));
 }
 // 16 bytes (or 4) from global to shared memory, asynchronously; `bytes` 0 writes zeros
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
@@ -399,7 +405,7 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm(D, NT)) cache8_attn_k
             for (int j = 0; j < 2; ++j) {
               const float top = column_max(fmaxf(s[nt][j], s[nt][j + 2])) * factor[nt][j];
               const float m_old = m_run[nt][j], mv_old = mv_run[nt][j];
-              const float m = fmaxf(m_old, top), mv = fmaxf(mv_old, top + vexp);
+              const float m = fmaxf(m_old, ceilf(top)), mv = fmaxf(mv_old, ceilf(top) + vexp);
               float fv = ex2(mv_old - mv);
               if (PAIR) {  // columns 4-7 go with 0-3
                 const float other = __shfl_xor_sync(0xffffffffu, fv, 2);
@@ -511,10 +517,10 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm(D, NT)) cache8_attn_k
       for (int w = 0; w < kWarps; ++w) m = fmaxf(m, s_m[w][tid]), mv = fmaxf(mv, s_mv[w][tid]);
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) l = __fmaf_rn(s_l[w][tid], ex2(s_m[w][tid] - m), l);
-      const float f = !whole ? 1.0f : l > 0.0f ? ex2(mv - m - kShift) / l : 0.0f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) s_w[w][tid] = ex2(s_mv[w][tid] - mv) * f;
-      s_fin[tid][0] = m, s_fin[tid][1] = mv, s_fin[tid][2] = l;
+      for (int w = 0; w < kWarps; ++w) s_w[w][tid] = ex2(s_mv[w][tid] - mv);
+      const float2 last = last_factor(mv - m - kShift, l);
+      s_fin[tid][0] = whole ? last.x : m, s_fin[tid][1] = whole ? last.y : mv, s_fin[tid][2] = l;
       if (MASS && whole && rt * R + tid < rows) a.stats[first + rt * R + tid] = make_float2(m, l > 0.0f ? 1.0f / l : 0.0f);
     }
     __syncthreads();
@@ -534,6 +540,10 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm(D, NT)) cache8_attn_k
         }
         const float f = s_w[w][r];
         acc.x = __fmaf_rn(v.x, f, acc.x), acc.y = __fmaf_rn(v.y, f, acc.y), acc.z = __fmaf_rn(v.z, f, acc.z), acc.w = __fmaf_rn(v.w, f, acc.w);
+      }
+      if (whole) {
+        const float f0 = s_fin[r][0], f1 = s_fin[r][1];
+        acc.x = acc.x * f0 * f1, acc.y = acc.y * f0 * f1, acc.z = acc.z * f0 * f1, acc.w = acc.w * f0 * f1;
       }
       float* to = whole ? a.out + (row0 + r * step) * D + ch : part + r * (D + 4) + 4 + ch;
       *reinterpret_cast<float4*>(to) = acc;
@@ -584,9 +594,9 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm(D, NT)) cache8_attn_k
           m = m2, mv = mv2;
         }
         const long long row = first + (long long)(rt * R + r) * step;
-        const float f = l > 0.0f ? ex2(mv - m - kShift) / l : 0.0f;
+        const float2 last = last_factor(mv - m - kShift, l);
 #pragma unroll
-        for (int j = 0; j < D / 32; ++j) a.out[row * D + 32 * j + lane] = acc[j] * f;
+        for (int j = 0; j < D / 32; ++j) a.out[row * D + 32 * j + lane] = acc[j] * last.x * last.y;
         if (MASS && lane == 0) a.stats[row] = make_float2(m, l > 0.0f ? 1.0f / l : 0.0f);
       }
     }
@@ -625,7 +635,8 @@ __global__ void __launch_bounds__(D) cache8_combine_kernel(Cache8AttnArgs a, boo
     m = m2, mv = mv2;
   }
   const long long row = tail.row0 + (long long)r * tail.step;
-  a.out[row * D + ch] = l > 0.0f ? acc * ex2(mv - m - kShift) / l : 0.0f;
+  const float2 last = last_factor(mv - m - kShift, l);
+  a.out[row * D + ch] = acc * last.x * last.y;
   if (mass && ch == 0) a.stats[row] = make_float2(m, l > 0.0f ? 1.0f / l : 0.0f);
 }
 
@@ -682,12 +693,12 @@ __global__ void __launch_bounds__(kCombineWarps * 32) cache8_combine_many_kernel
   for (int j = 0; j < N; ++j) s_o[warp][N * lane + j] = acc[j];
   __syncthreads();
   const long long row = tail.row0 + (long long)r * tail.step;
-  const float f = l > 0.0f ? ex2(mv - m - kShift) / l : 0.0f;
+  const float2 last = last_factor(mv - m - kShift, l);
   for (int ch = tid; ch < D; ch += kCombineWarps * 32) {
     float sum = 0.0f;
 #pragma unroll
     for (int w = 0; w < kCombineWarps; ++w) sum += s_o[w][ch];
-    a.out[row * D + ch] = sum * f;
+    a.out[row * D + ch] = sum * last.x * last.y;
   }
   if (mass && tid == 0) a.stats[row] = make_float2(m, l > 0.0f ? 1.0f / l : 0.0f);
 }

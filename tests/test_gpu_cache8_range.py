@@ -1,0 +1,64 @@
+"""Attention over the 8-bit cache where scores, value scales and codes lie far apart, against the fp64 oracle.
+
+The caches are written by hand: channel 0 of the keys separates the scores, and values and their
+scales are set block by block.  The tolerance is that of tests/test_gpu_cache8.py, and half a step of
+fp32's subnormals, 2^-150, for each of the three roundings that a subnormal result can meet."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import cache8 as o8
+from quantization_cg_encode_b200 import cg
+from tests.gpu_util import bf16_np, need_gpu
+from tests.test_gpu_cache8 import Cache, _attend
+
+pytestmark = pytest.mark.gpu
+
+# (B, H, T, rows of a KV head): a unit that one CTA takes, one for a cluster, one that equal runs cut
+# into many pieces, many units in runs, and runs that cut units into few pieces
+SHAPES = [(1, 1, 128, 4), (1, 1, 2048, 4), (1, 1, 24576, 2), (45, 8, 256, 3), (40, 8, 1056, 8), (2, 1, 2048, 16)]
+
+
+def _byte(v, code):
+    return o8.encode(np.asarray(v, np.float64), code)
+
+
+def _cache(B, H, T, d, code, tb=16):
+    """Keys zero, values zero, all scales 1."""
+    c = Cache(1, B, H, T, d, code, tb)
+    c.codes[:] = 0
+    c.scales[:] = 1
+    return c
+
+
+def _queries(B, H, rows, d):
+    """1 in channel 0: a token's score is its key's channel 0 times the call's scale."""
+    q = torch.zeros((1, B, H * rows, 1, d), dtype=torch.bfloat16)
+    q[..., 0] = 1
+    return q
+
+
+def _check(c, q, lens, scale):
+    scale = float(np.float32(scale))
+    got = _attend(c, q, lens, scale=scale)
+    ref, _, spread, big = o8.attention(bf16_np(q), c.codes, c.scales, lens, c.code, c.tb, scale)
+    eps = big[..., None] * (c.dims[4] / 16 + 4) * 2.0 ** -23 + 40 * 2.0 ** -22
+    err, tol = np.abs(got - ref), 2 * eps * spread + 3 * 2.0 ** -150
+    assert (err <= tol).all(), "worst %.3g of its tolerance" % np.nanmax(err / tol)
+    return ref
+
+
+@pytest.mark.parametrize("code", [cg.CACHE8_INT8, cg.CACHE8_E4M3])
+@pytest.mark.parametrize("B,H,T,rows", SHAPES)
+def test_outputs_near_the_least_normal_number(B, H, T, rows, code):
+    """Values stored at the least scale give outputs that fp32 holds, whatever the scores are."""
+    need_gpu()
+    d = 64
+    c = _cache(B, H, T, d, code)
+    rng = np.random.default_rng(T)
+    c.codes[:, 0, ..., 0] = _byte(rng.integers(-8, 9, (B, H, T)), code)
+    c.codes[:, 1] = _byte(rng.integers(1, 16, (B, H, T, d)), code)
+    c.scales[:, 1] = 2.0 ** -126
+    c.up()
+    ref = _check(c, _queries(B, H, rows, d), [T - 3] * B, 0.25)
+    assert ref.min() > 2.0 ** -126 and ref.max() < 1e-36
