@@ -429,10 +429,10 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm(D, NT)) cache8_attn_k
             const float p0 = ex2(x[nt][j]), p1 = ex2(x[nt][j + 2]);
             tile_sum[2 * nt + j] = p0 + p1;
             l_run[nt][j] += tile_sum[2 * nt + j];
-            // p s_V relative to M': p 2^f <= 2^(kLag + kShift), so a factor of over 2^100 meets a p below 2^-85, whose
-            // row's sum holds a weight of 1 at least: nothing that a result in fp32 could show
-            const float f = ex2(fminf((vexp + kShift) - mv_m[nt][j], 100.0f));
-            pv[j] = p0 * f, pv[j + 2] = p1 * f;
+            // p s_V relative to M' has an exponential of its own: p times 2^e would be nothing where fp32 has lost p,
+            // yet such a token is the row's output where the tokens of weight have values of a far smaller scale
+            const float e = (vexp + kShift) - mv_m[nt][j];
+            pv[j] = ex2(x[nt][j] + e), pv[j + 2] = ex2(x[nt][j + 2] + e);
           }
 #pragma unroll
           for (int j = 0; j < 2; ++j) {

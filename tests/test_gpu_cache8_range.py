@@ -3,6 +3,8 @@
 The caches are written by hand: channel 0 of the keys separates the scores, and values and their
 scales are set block by block.  The tolerance is that of tests/test_gpu_cache8.py, and half a step of
 fp32's subnormals, 2^-150, for each of the three roundings that a subnormal result can meet."""
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -62,3 +64,21 @@ def test_outputs_near_the_least_normal_number(B, H, T, rows, code):
     c.up()
     ref = _check(c, _queries(B, H, rows, d), [T - 3] * B, 0.25)
     assert ref.min() > 2.0 ** -126 and ref.max() < 1e-36
+
+
+@pytest.mark.parametrize("code", [cg.CACHE8_INT8, cg.CACHE8_E4M3])
+@pytest.mark.parametrize("B,H,T,rows", SHAPES)
+@pytest.mark.parametrize("gap,light,value", [(95, 0, 0), (110, 100, 0), (95, 120, 96), (120, 110, 0), (140, 120, 1)])
+def test_light_tokens_with_the_larger_value_scales_are_the_output(B, H, T, rows, gap, light, value, code):
+    """Half of the blocks draw all of the weight and hold values of the least scale, the others have
+    weights 2^-gap and the scale 2^light: the output is theirs."""
+    need_gpu()
+    d = 64
+    c = _cache(B, H, T, d, code)
+    heavy = np.random.default_rng(T + gap).random((1, B, H, T // 16)) < 0.5
+    heavy[..., 0], heavy[..., 1] = True, False
+    c.codes[:, 0, ..., 0] = np.where(np.repeat(heavy, 16, -1), _byte(96, code), 0)
+    c.codes[:, 1] = np.where(np.repeat(heavy, 16, -1)[..., None], _byte(value, code), _byte(96, code))
+    c.scales[:, 1] = np.where(heavy, 2.0 ** -126, 2.0 ** light)
+    c.up()
+    _check(c, _queries(B, H, rows, d), [T - 3] * B, gap * math.log(2) / 96)
