@@ -418,9 +418,11 @@ cg_status cg_cache8_attention_workspace_size(const cg_kv_desc* kv, const cg_cach
  *             CG_ERR_UNSUPPORTED)
  *   workspace_dev / workspace_bytes: at least cg_cache8_attention_workspace_size(); nothing
  *             in it outlives the call
- * Scores, maxima and sums are fp32; the softmax weights enter the product with the values
- * as two fp16 terms (2^-22).  Scales have to be powers of two, as cg_cache8_append
- * writes them. */
+ * Scores, maxima and sums are fp32.  Two operands are fp16 terms: the query, times a power of
+ * two of its row (an element is exact or off by 2^-39 of its row's largest), and the weights
+ * times the value scale, p s_V, two terms (off by 2^-22 of itself or, where that is more, 2^-37
+ * of its row's largest p s_V).  Scales have to be powers of two, as cg_cache8_append writes
+ * them. */
 cg_status cg_cache8_attention(const cg_kv_desc* kv, const cg_cache8_desc* c8, const cg_cache8_attn_desc* at,
                               const void* q_dev, const uint8_t* codes_dev, const float* scales_dev, const int32_t* lens_dev,
                               const int32_t* sel_dev, float* out_dev, float* mass_dev, void* workspace_dev,

@@ -10,18 +10,23 @@
 // fifth-generation MMA would leave 120 of its 128 rows empty, and this pass waits for memory).
 //   scores  A = 16 tokens x 16 channels of key codes, exact in fp16; B = q, times a power of two
 //           per row that puts its largest element into [2^14, 2^15): bf16 values are exact in
-//           fp16 down to 2^-29 of the row's largest;
-//   values  A = 16 channels x 16 tokens of value codes; B = p as two fp16 terms (2^-22), which are
-//           two products, or, for up to four rows (PAIR), columns 0-3 and 4-7 of one.
+//           fp16 down to 2^-31 of the row's largest;
+//   values  A = 16 channels x 16 tokens of value codes; B = p s_V as two fp16 terms, which are two
+//           products, or, for up to four rows (PAIR), columns 0-3 and 4-7 of one, the second term
+//           times 2^11.  A weight is off by at most 2^-22 of itself or, where that is more, 2^-37
+//           (PAIR: 2^-48) of its row's largest p s_V: half a step of fp16's subnormals.  (Three
+//           bf16 terms, which keep all bits of every weight, took 53 us where these take 48, and 85
+//           with 16 rows where these take 73.)
 // The order of channels within a contraction is free, so ldmatrix moves the bytes as 16-bit
 // pairs and no thread exchanges codes with another; B of the second product is the scores'
 // layout transposed (movmatrix).
 //
 // The value scale is a power of two, 2^v: p s_V = 2^(x + v) is kept relative to its own running
-// maximum M', so that no ratio of scales costs fp16 range, and the sum of p relative to M:
+// maximum M', so that a row's largest p s_V stands high in fp16's range whatever the scales are, and
+// the sum of p relative to M:
 //   out = (sum 2^(x + v - M') code) / (sum 2^(x - M)) 2^(M' - M).
 // M and M' are whole numbers, so that M' - M is exact; they follow the maxima lazily (they move when
-// a value is 2^8 above).
+// a value is 2^2 above).
 //
 // All tiles of the call (every unit's, a unit being the query rows of one layer, sequence and KV
 // head, 8 or 16 of them) stand in one row, of which every CTA takes an equal run, so that ragged
@@ -62,8 +67,12 @@ constexpr long long clusters_at_once(int size, int per_sm) {
 }
 constexpr float kNone = -1.0e30f;       // a running maximum that has seen nothing
 constexpr float kDeep = -80.0f;         // the least power of two that a result is multiplied with at once
-constexpr float kLag = 8.0f;            // how far a value may lie above the running maximum
-constexpr float kShift = 7.0f;          // 2^kShift p' <= 2^15 fits fp16
+// p' = 2^kShift p s_V relative to M' is at most 2^(kLag + kShift) = 2^15, as far as fp16 reaches, and the row's
+// largest at least 2^12: the farther up, the more bits the weights far below it keep (2^8 and 2^7 lost six, in
+// the same time)
+constexpr float kLag = 2.0f;            // how far a value may lie above the running maximum
+constexpr float kShift = 13.0f;
+constexpr float kLow = 2048.0f;         // what the second term is times where it has columns of its own
 
 __device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
   uint32_t r;
@@ -438,7 +447,8 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm(D, NT)) cache8_attn_k
           for (int j = 0; j < 2; ++j) {
             const __half2 hi = __floats2half2_rn(pv[2 * j], pv[2 * j + 1]);
             const float2 back = __half22float2(hi);
-            const __half2 lo = __floats2half2_rn(pv[2 * j] - back.x, pv[2 * j + 1] - back.y);
+            const float up = PAIR ? kLow : 1.0f;
+            const __half2 lo = __floats2half2_rn((pv[2 * j] - back.x) * up, (pv[2 * j + 1] - back.y) * up);
             if (PAIR) {
               const uint32_t other = __shfl_xor_sync(0xffffffffu, *reinterpret_cast<const uint32_t*>(&lo), 2);
               bhi[nt][j] = transpose_8x8(c < 2 ? *reinterpret_cast<const uint32_t*>(&hi) : other);
@@ -536,7 +546,8 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm(D, NT)) cache8_attn_k
         float4 v = *reinterpret_cast<const float4*>(&s_o[(w * R + r) * D + ch]);
         if (PAIR) {
           const float4 lo = *reinterpret_cast<const float4*>(&s_o[(w * R + r + 4) * D + ch]);
-          v.x += lo.x, v.y += lo.y, v.z += lo.z, v.w += lo.w;
+          constexpr float down = 1.0f / kLow;
+          v.x = __fmaf_rn(lo.x, down, v.x), v.y = __fmaf_rn(lo.y, down, v.y), v.z = __fmaf_rn(lo.z, down, v.z), v.w = __fmaf_rn(lo.w, down, v.w);
         }
         const float f = s_w[w][r];
         acc.x = __fmaf_rn(v.x, f, acc.x), acc.y = __fmaf_rn(v.y, f, acc.y), acc.z = __fmaf_rn(v.z, f, acc.z), acc.w = __fmaf_rn(v.w, f, acc.w);

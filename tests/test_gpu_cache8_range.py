@@ -2,7 +2,12 @@
 
 The caches are written by hand: channel 0 of the keys separates the scores, and values and their
 scales are set block by block.  The tolerance is that of tests/test_gpu_cache8.py, and half a step of
-fp32's subnormals, 2^-150, for each of the three roundings that a subnormal result can meet."""
+fp32's subnormals, 2^-150, for each of the three roundings that a subnormal result can meet.
+
+Where weights lie far below their row's largest p s_V, each may be off by 2^-37 of that instead: the
+weights' terms are fp16 numbers relative to it, which stands at 2^12 at least, and half a step of
+fp16's subnormals is 2^-25 (up to four rows: of the second term, which is times 2^11 there: 2^-48).  A
+value code c of such a token turns that into |c| 2^-37 max(p s_V)."""
 import math
 
 import numpy as np
@@ -40,12 +45,19 @@ def _queries(B, H, rows, d):
     return q
 
 
-def _check(c, q, lens, scale):
+def _check(c, q, lens, scale, far=False):
     scale = float(np.float32(scale))
     got = _attend(c, q, lens, scale=scale)
     ref, _, spread, big = o8.attention(bf16_np(q), c.codes, c.scales, lens, c.code, c.tb, scale)
     eps = big[..., None] * (c.dims[4] / 16 + 4) * 2.0 ** -23 + 40 * 2.0 ** -22
     err, tol = np.abs(got - ref), 2 * eps * spread + 3 * 2.0 ** -150
+    if far:  # the rows of a KV head are the same
+        n, (_, B, H, T, d) = lens[0], c.dims
+        s = o8.decode(c.codes[0, 0, :, :, :n, 0], c.code) * scale
+        w = np.exp(s - s.max(-1, keepdims=True))
+        largest = (w / w.sum(-1, keepdims=True) * np.repeat(c.scales[0, 1], c.tb, -1)[..., :n]).max(-1)
+        low = 2.0 ** (-48 if q.shape[2] // H <= 4 else -37) * largest[..., None] * np.abs(o8.decode(c.codes[0, 1, :, :, :n], c.code)).sum(2)  # [B, H, d]
+        tol = tol + np.repeat(low, q.shape[2] // H, 1)[None, :, :, None]
     assert (err <= tol).all(), "worst %.3g of its tolerance" % np.nanmax(err / tol)
     return ref
 
@@ -82,3 +94,57 @@ def test_light_tokens_with_the_larger_value_scales_are_the_output(B, H, T, rows,
     c.scales[:, 1] = np.where(heavy, 2.0 ** -126, 2.0 ** light)
     c.up()
     _check(c, _queries(B, H, rows, d), [T - 3] * B, gap * math.log(2) / 96)
+
+
+@pytest.mark.parametrize("code", [cg.CACHE8_INT8, cg.CACHE8_E4M3])
+@pytest.mark.parametrize("B,H,T,rows", SHAPES)
+@pytest.mark.parametrize("ratio", [12, 20, 33, 34, 35, 60])
+def test_channels_that_only_blocks_of_small_scales_reach(B, H, T, rows, ratio, code):
+    """One value block has a scale 2^ratio times the others' and codes in one channel only: the other
+    channels are the other blocks'."""
+    need_gpu()
+    d = 64
+    c = _cache(B, H, T, d, code)
+    rng = np.random.default_rng(T + ratio)
+    c.codes[:, 0, ..., 0] = _byte(rng.integers(-8, 9, (B, H, T)), code)
+    c.codes[:, 1] = _byte(rng.integers(0, 16, (B, H, T, d)), code)
+    c.codes[:, 1, :, :, 16:32] = 0
+    c.codes[:, 1, :, :, 16:32, 5] = _byte(96, code)
+    c.scales[:, 1, :, :, 1] = 2.0 ** ratio
+    c.up()
+    _check(c, _queries(B, H, rows, d), [T - 3] * B, 0.25, far=True)
+
+
+@pytest.mark.parametrize("code", [cg.CACHE8_INT8, cg.CACHE8_E4M3])
+@pytest.mark.parametrize("B,H,T,rows", SHAPES)
+@pytest.mark.parametrize("gap", [12.4, 20.4, 31.4, 33.4, 34.4, 35.4, 60.4])
+def test_channels_that_only_light_tokens_reach(B, H, T, rows, gap, code):
+    """One token has 2^gap times the others' weights and codes in the even channels only: the odd
+    channels are the other tokens', those of its own tile among them."""
+    need_gpu()
+    d = 64
+    c = _cache(B, H, T, d, code)
+    rng = np.random.default_rng(T + int(gap))
+    c.codes[:, 0, :, :, 21, 0] = _byte(96, code)
+    c.codes[:, 1] = _byte(rng.integers(0, 16, (B, H, T, d)), code)
+    c.codes[:, 1, :, :, 21, 1::2] = 0
+    c.up()
+    _check(c, _queries(B, H, rows, d), [T - 3] * B, gap * math.log(2) / 96, far=True)
+
+
+@pytest.mark.parametrize("code", [cg.CACHE8_INT8, cg.CACHE8_E4M3])
+@pytest.mark.parametrize("d,rows", [(64, 4), (128, 16)])
+def test_queries_with_an_element_far_above_the_others(d, rows, code):
+    """One element 2^30, the others down to 1/2, and keys that are zero where it is: exact down to 2^-31
+    of the row's largest, so the scores are the others'."""
+    need_gpu()
+    B, H, T = 2, 2, 256
+    c = _cache(B, H, T, d, code)
+    rng = np.random.default_rng(d)
+    c.codes[:, :, :, :, :, 1:] = _byte(rng.integers(-15, 16, (1, 2, B, H, T, d - 1)), code)
+    c.up()
+    q = _queries(B, H, rows, d)
+    q[..., 0] = 2.0 ** 30
+    x = torch.from_numpy(rng.uniform(0.5, 4, q[..., 1:].shape) * rng.choice([-1.0, 1.0], q[..., 1:].shape))
+    q[..., 1:] = x.to(torch.bfloat16)
+    _check(c, q, [T, T - 39], 2.0 ** -7)
