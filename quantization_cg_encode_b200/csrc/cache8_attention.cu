@@ -56,8 +56,7 @@ constexpr int ctas_per_sm(int d, int nt) { return d == 128 && nt == 2 ? 1 : 2; }
 constexpr int kStages = 3;
 constexpr int kSms = 148;               // what the number of CTAs is sized for
 constexpr int kLeastRun = 8;            // tiles of a run at least
-constexpr int kCombineWarps = 8;
-constexpr int kFewPieces = 4;            // of a unit: read one after another
+constexpr int kFewPieces = 4;            // of a unit that are read one after another
 constexpr int kMaxCluster = 8;
 constexpr int kClusterTiles = 16;       // tiles of a warp in a unit that a cluster takes
 // Clusters of a size that the GPU holds at once, at one or two CTAs an SM: its parts' numbers of SMs are no
@@ -624,40 +623,16 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm(D, NT)) cache8_attn_k
   }
 }
 
-// The units whose pieces lie in several runs: piece by piece from the run in which the unit ends
-// back to the one in which it begins.  One CTA a run and row.
-template <int D>
-__global__ void __launch_bounds__(D) cache8_combine_kernel(Cache8AttnArgs a, bool mass) {
-  const int R = 8 * a.nt, ch = threadIdx.x, r = blockIdx.y;
-  previous_kernel_done();
-  dependents_may_launch();
-  const Tail tail = reinterpret_cast<const Tail*>(a.tails)[blockIdx.x];
-  if (r >= tail.rows || tail.pieces == 0) return;
-  auto piece = [&](int i) {  // 0: the last
-    return a.part + ((long long)(blockIdx.x - i) * 2 + (i ? 1 : 0)) * R * (D + 4) + r * (D + 4);
-  };
-  float m = kNone, mv = kNone, l = 0.0f, acc = 0.0f;
-  for (int i = 0; i < tail.pieces; ++i) {
-    const float4 st = *reinterpret_cast<const float4*>(piece(i));
-    const float v = piece(i)[4 + ch];
-    const float m2 = fmaxf(m, st.x), mv2 = fmaxf(mv, st.y);
-    l = l * ex2(m - m2) + st.z * ex2(st.x - m2);
-    acc = acc * ex2(mv - mv2) + v * ex2(st.y - mv2);
-    m = m2, mv = mv2;
-  }
-  const long long row = tail.row0 + (long long)r * tail.step;
-  const float2 last = last_factor(mv - m - kShift, l);
-  a.out[row * D + ch] = acc * last.x * last.y;
-  if (mass && ch == 0) a.stats[row] = make_float2(m, l > 0.0f ? 1.0f / l : 0.0f);
-}
-
-// The same where a unit may be cut into as many pieces as there are CTAs: they are read side by side, first all
-// maxima and sums, a piece a thread, then the outputs, which the warps take in turn.  (One head of 32768
-// tokens, 256 pieces: 16 us in all, 57 with the kernel above.)
-template <int D>
-__global__ void __launch_bounds__(kCombineWarps * 32) cache8_combine_many_kernel(Cache8AttnArgs a, bool mass) {
+// The units whose pieces lie in several runs, from the run in which a unit ends back to the one in
+// which it begins.  One CTA a run and row.  How many pieces there are is known here alone (lengths
+// live on the device, and a batch may hold one long sequence beside vacant slots).  A few are read one
+// after another, a channel a thread; more side by side, first all maxima and sums, a piece a thread,
+// then the outputs, which the warps take in turn.  (One head of 32768 tokens, 256 pieces, alone or
+// beside 79 vacant slots: 16 us with the attention, 57 one after another.)
+template <int D, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32) cache8_combine_kernel(Cache8AttnArgs a, bool mass) {
   constexpr int N = D / 32;
-  __shared__ float s_stat[kCombineWarps][3], s_o[kCombineWarps][D];
+  __shared__ float s_stat[WARPS][3], s_o[WARPS][D];
   const int R = 8 * a.nt, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = blockIdx.y;
   previous_kernel_done();
   dependents_may_launch();
@@ -666,9 +641,26 @@ __global__ void __launch_bounds__(kCombineWarps * 32) cache8_combine_many_kernel
   auto piece = [&](int i) {  // 0: the last
     return a.part + ((long long)(blockIdx.x - i) * 2 + (i ? 1 : 0)) * R * (D + 4) + r * (D + 4);
   };
-  // a thread's pieces, then a warp's, then all: m, m' and the sum relative to m
+  const long long row = tail.row0 + (long long)r * tail.step;
   float m = kNone, mv = kNone, l = 0.0f;
-  for (int i = tid; i < tail.pieces; i += kCombineWarps * 32) {
+  if (tail.pieces <= kFewPieces) {
+    if (tid >= D) return;
+    float acc = 0.0f;
+    for (int i = 0; i < tail.pieces; ++i) {
+      const float4 st = *reinterpret_cast<const float4*>(piece(i));
+      const float v = piece(i)[4 + tid];
+      const float m2 = fmaxf(m, st.x), mv2 = fmaxf(mv, st.y);
+      l = l * ex2(m - m2) + st.z * ex2(st.x - m2);
+      acc = acc * ex2(mv - mv2) + v * ex2(st.y - mv2);
+      m = m2, mv = mv2;
+    }
+    const float2 last = last_factor(mv - m - kShift, l);
+    a.out[row * D + tid] = acc * last.x * last.y;
+    if (mass && tid == 0) a.stats[row] = make_float2(m, l > 0.0f ? 1.0f / l : 0.0f);
+    return;
+  }
+  // a thread's pieces, then a warp's, then all: m, m' and the sum relative to m
+  for (int i = tid; i < tail.pieces; i += WARPS * 32) {
     const float4 st = *reinterpret_cast<const float4*>(piece(i));
     const float m2 = fmaxf(m, st.x);
     l = l * ex2(m - m2) + st.z * ex2(st.x - m2);
@@ -682,14 +674,14 @@ __global__ void __launch_bounds__(kCombineWarps * 32) cache8_combine_many_kernel
   __syncthreads();
   m = mv = kNone, l = 0.0f;
 #pragma unroll
-  for (int w = 0; w < kCombineWarps; ++w) m = fmaxf(m, s_stat[w][0]), mv = fmaxf(mv, s_stat[w][1]);
+  for (int w = 0; w < WARPS; ++w) m = fmaxf(m, s_stat[w][0]), mv = fmaxf(mv, s_stat[w][1]);
 #pragma unroll
-  for (int w = 0; w < kCombineWarps; ++w) l = __fmaf_rn(s_stat[w][2], ex2(s_stat[w][0] - m), l);
+  for (int w = 0; w < WARPS; ++w) l = __fmaf_rn(s_stat[w][2], ex2(s_stat[w][0] - m), l);
   float acc[N];
 #pragma unroll
   for (int j = 0; j < N; ++j) acc[j] = 0.0f;
 #pragma unroll 8
-  for (int i = warp; i < tail.pieces; i += kCombineWarps) {
+  for (int i = warp; i < tail.pieces; i += WARPS) {
     const float* v = piece(i);
     const float f = ex2(v[1] - mv);
     if constexpr (N == 4) {
@@ -703,12 +695,11 @@ __global__ void __launch_bounds__(kCombineWarps * 32) cache8_combine_many_kernel
 #pragma unroll
   for (int j = 0; j < N; ++j) s_o[warp][N * lane + j] = acc[j];
   __syncthreads();
-  const long long row = tail.row0 + (long long)r * tail.step;
   const float2 last = last_factor(mv - m - kShift, l);
-  for (int ch = tid; ch < D; ch += kCombineWarps * 32) {
+  for (int ch = tid; ch < D; ch += WARPS * 32) {
     float sum = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kCombineWarps; ++w) sum += s_o[w][ch];
+    for (int w = 0; w < WARPS; ++w) sum += s_o[w][ch];
     a.out[row * D + ch] = sum * last.x * last.y;
   }
   if (mass && tid == 0) a.stats[row] = make_float2(m, l > 0.0f ? 1.0f / l : 0.0f);
@@ -844,9 +835,11 @@ cudaError_t launch_d(const Cache8AttnArgs& a, cudaStream_t st) {
   if (e != cudaSuccess || a.cluster) return e;
   const int rows = a.n_select ? a.gq : a.gq * a.nq;
   const dim3 grid(a.ctas, rows < 8 * a.nt ? rows : 8 * a.nt);
-  // pieces of a unit, were all of one length
-  if (a.ctas <= kFewPieces * units(a)) return launch_after(cache8_combine_kernel<D>, grid, D, 0, st, 1, a, a.mass != nullptr);
-  return launch_after(cache8_combine_many_kernel<D>, grid, kCombineWarps * 32, 0, st, 1, a, a.mass != nullptr);
+  // Eight warps for the merge where sequences of one length, or one that alone holds tokens, are cut into many pieces.
+  // (One head of 32768 tokens: eight 16 us, four 27; eight heads 21.8, 22.5; 512 units of 64 ragged sequences 114.2, 113.8;
+  // 96 units of 16 rows 73.8, 73.2.)
+  const bool many = a.ctas > kFewPieces * units(a) || a.ctas > 64 * (units(a) / a.c.k.B);
+  return launch_after(many ? cache8_combine_kernel<D, 8> : cache8_combine_kernel<D, 4>, grid, many ? 256 : 128, 0, st, 1, a, a.mass != nullptr);
 }
 
 int mass_chunks(const Cache8AttnArgs& a) { return (a.c.blocks() + 31) / 32; }

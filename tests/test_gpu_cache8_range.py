@@ -1,6 +1,6 @@
-"""Attention over the 8-bit cache where scores, value scales and codes lie far apart, against the fp64 oracle.
+"""Attention over the 8-bit cache where scores, value scales, codes and lengths lie far apart, against the fp64 oracle.
 
-The caches are written by hand: channel 0 of the keys separates the scores, and values and their
+Most caches are written by hand: channel 0 of the keys separates the scores, and values and their
 scales are set block by block.  The tolerance is that of tests/test_gpu_cache8.py, and half a step of
 fp32's subnormals, 2^-150, for each of the three roundings that a subnormal result can meet.
 
@@ -17,7 +17,7 @@ import torch
 from oracle import cache8 as o8
 from quantization_cg_encode_b200 import cg
 from tests.gpu_util import bf16_np, need_gpu
-from tests.test_gpu_cache8 import Cache, _attend
+from tests.test_gpu_cache8 import Cache, _attend, _check_attention, _close, _new
 
 pytestmark = pytest.mark.gpu
 
@@ -148,3 +148,26 @@ def test_queries_with_an_element_far_above_the_others(d, rows, code):
     x = torch.from_numpy(rng.uniform(0.5, 4, q[..., 1:].shape) * rng.choice([-1.0, 1.0], q[..., 1:].shape))
     q[..., 1:] = x.to(torch.bfloat16)
     _check(c, q, [T, T - 39], 2.0 ** -7)
+
+
+@pytest.mark.parametrize("code", [cg.CACHE8_INT8, cg.CACHE8_E4M3])
+@pytest.mark.parametrize("B,H,d,gq,nq,live", [(80, 1, 128, 4, 1, 0), (80, 1, 64, 2, 3, 41), (24, 2, 128, 8, 2, 23), (12, 8, 64, 4, 1, 5)])
+def test_one_long_sequence_beside_vacant_slots(B, H, d, gq, nq, live, code):
+    """All runs are pieces of its few units, although the batch has many; a short one at the other end."""
+    need_gpu()
+    T, tb = 8192, 64
+    lens = [0] * B
+    lens[live], lens[B - 1 - live] = T - 9, 70
+    c = Cache(1, B, H, T, d, code, tb)
+    rng = np.random.default_rng(B + d)
+    for b in (live, B - 1 - live):
+        c.codes[0, :, b, :, :lens[b]] = _byte(rng.integers(-60, 61, (2, H, lens[b], d)), code)
+        c.scales[0, :, b] = 2.0 ** rng.integers(-9, -5, (2, H, T // tb))
+    c.up()
+    q = _new(torch.Generator().manual_seed(B), 1, B, H * gq, nq, d)
+    ref, want, spread, big = _check_attention(c, q, lens)
+    eps = big.max() * (d / 16 + 4) * 2.0 ** -23 + 40 * 2.0 ** -22
+    mass = torch.full((1, B, H, T // tb), 7.0, dtype=torch.float32, device="cuda")
+    got = _attend(c, q, lens, mass=mass)
+    _close(got, ref, spread, big, d)
+    assert np.all(np.abs(mass.cpu().numpy().astype(np.float64) - want) <= 2 * eps * want)
