@@ -171,3 +171,25 @@ def test_one_long_sequence_beside_vacant_slots(B, H, d, gq, nq, live, code):
     got = _attend(c, q, lens, mass=mass)
     _close(got, ref, spread, big, d)
     assert np.all(np.abs(mass.cpu().numpy().astype(np.float64) - want) <= 2 * eps * want)
+
+
+@pytest.mark.parametrize("code", [cg.CACHE8_INT8, cg.CACHE8_E4M3])
+@pytest.mark.parametrize("B,H,d,gq,nq", [(8, 8, 128, 4, 1), (9, 8, 64, 3, 4), (3, 6, 128, 8, 2), (40, 8, 64, 2, 1)])
+def test_short_sequences_in_a_call_for_long_ones(B, H, d, gq, nq, code):
+    """The work is laid out for lengths that the sequences do not have."""
+    need_gpu()
+    T, tb = 20480, 16
+    lens = [(1, 16, 40, 0, 17, 33, 5, 130)[b % 8] for b in range(B)]
+    c = Cache(1, B, H, T, d, code, tb)
+    rng = np.random.default_rng(B + d)
+    n = 144
+    c.codes[:, :, :, :, :n] = _byte(rng.integers(-60, 61, (1, 2, B, H, n, d)), code)
+    c.scales[..., :n // tb] = 2.0 ** rng.integers(-9, -5, (1, 2, B, H, n // tb))
+    c.up()
+    q = _new(torch.Generator().manual_seed(B), 1, B, H * gq, nq, d)
+    ref, want, spread, big = _check_attention(c, q, lens)
+    eps = big.max() * (d / 16 + 4) * 2.0 ** -23 + 40 * 2.0 ** -22
+    mass = torch.full((1, B, H, T // tb), 7.0, dtype=torch.float32, device="cuda")
+    got = _attend(c, q, lens, mass=mass)
+    _close(got, ref, spread, big, d)
+    assert np.all(np.abs(mass.cpu().numpy().astype(np.float64) - want) <= 2 * eps * want)
