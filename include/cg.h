@@ -450,7 +450,7 @@ cg_status cg_cache8_select_workspace_size(const cg_kv_desc* kv, const cg_cache8_
  * scores.  With q8 = rnd(q / 2^e) a query row in whole numbers, e the least with
  * |q| <= 127 2^e, a block's score is
  *   max over the KV head's query heads of  2^e s_K sum_c max(q8_c lo_c, q8_c hi_c),
- * exact in fp32; ties go to the lowest block.
+ * exact in fp32 within its normal range; ties go to the lowest block.
  *   q_dev, scales_dev, bounds_dev, lens_dev  as above (input)
  *   sel_dev  int32 [n_layers][B][H][q_tokens][n_select] (output): block indices, ascending,
  *            then -1 where the token sees fewer than n_select blocks */

@@ -12,8 +12,8 @@
 // eight in flight); a lane has the same eight channels of every second (fourth) token, so the
 // extremes of its channels are packed bf16 operations on the input as it is, and everything else
 // that needs them, the block's maximum and the bounds, comes from those: the rounding keeps order.
-// Registers are held to eight CTAs an SM, which the loads in flight need (five: 150 us, ten, with
-// spills: 166 us, where eight took 132).
+// Registers are held to eight CTAs an SM, which the loads in flight need, at 16 bytes of spills for
+// d = 128 (five CTAs: 150 us, ten: 166 us, where eight took 132).
 // Measured (B200, d = 128): 4096 tokens to 32 layers of 8 heads, 268 M values, 118 us = 6.9 TB/s of
 // the 3 bytes a value (the last writes stay in L2); one token of 8 sequences to the same layers
 // 4.8 us, latency.

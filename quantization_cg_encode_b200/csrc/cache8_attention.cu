@@ -38,9 +38,11 @@
 //
 // Measured (B200, d = 128, 4 query heads a KV head): 32 layers x 8 heads of 4096 tokens, int8,
 // 48 us = 5.6 TB/s; 64 ragged sequences of up to 8192 tokens, e4m3, 114 us = 5.9 TB/s.  A tile costs
-// 377 instructions of a warp, of which the codes' conversion is 174 (int8) and products 16.  With
-// 16 rows the products (48 a tile) and the other 460 instructions share the issue slots, which
-// bound it: 32 rows, 12 sequences of up to 16001 tokens, 71 us with block weights, 1.7 TB/s.
+// 382 instructions of a warp, of which the codes' conversion is 174 (int8) and products 16.  With
+// 16 rows it is 48 products and 470 others, and what bounds it is their latency: the registers leave
+// two warps a scheduler, which do not cover the chain from ldmatrix over conversion, product,
+// exponential and transposition to the second product (46% of the issue slots, 36% of the tensor
+// pipe, 28% of DRAM); 32 rows, 12 sequences of up to 16001 tokens, 73 us with block weights, 1.6 TB/s.
 #include <cooperative_groups.h>
 
 #include "cache8.cuh"
@@ -50,7 +52,8 @@ namespace cg {
 namespace {
 
 constexpr int kWarps = 8;
-// CTAs an SM: 16 query rows at d = 128 leave registers for one.  (With their q in shared memory 12
+// CTAs an SM: 16 query rows at d = 128 leave registers for one (at d = 64, without block weights, two
+// spill 44 to 56 bytes).  (With their q in shared memory 12
 // and 16 warps fit; four draft tokens with block weights took 74 us with 8, 88 with 12, 96 with 16.)
 constexpr int ctas_per_sm(int d, int nt) { return d == 128 && nt == 2 ? 1 : 2; }
 constexpr int kStages = 3;
@@ -59,8 +62,9 @@ constexpr int kLeastRun = 8;            // tiles of a run at least, if units hav
 constexpr int kFewPieces = 4;            // of a unit that are read one after another
 constexpr int kMaxCluster = 8;
 constexpr int kClusterTiles = 16;       // tiles of a warp in a unit that a cluster takes
-// Clusters of a size that the GPU holds at once, at one or two CTAs an SM: its parts' numbers of SMs are no
-// multiples of 4 or 8.  (16 units on 8 CTAs each, one an SM, took two turns: 17.2 us, on 4 each 10.2.)
+// Clusters of a size that a B200 holds at once, at one or two CTAs an SM: its parts' numbers of SMs are no
+// multiples of 4 or 8.  Constants, because the workspace size is asked for without a device; where fewer fit, the
+// others wait their turn.  (16 units on 8 CTAs each, one an SM, took two turns: 17.2 us, on 4 each 10.2.)
 constexpr long long clusters_at_once(int size, int per_sm) {
   return size == 8 ? (per_sm == 2 ? 33 : 15) : size == 4 ? (per_sm == 2 ? 71 : 33) : kSms / size * per_sm;
 }

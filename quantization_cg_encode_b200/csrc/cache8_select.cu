@@ -6,8 +6,8 @@
 //   2^e s_K sum_c max(q8_c lo_c, q8_c hi_c) = 2^e s_K (sum q8+ hi + sum q8- lo),
 // the largest product that keys between the block's bounds can have with the rounded row; a
 // block's score for a query token is its largest over the query heads of the KV head.  The sums
-// are whole numbers below 2^21 and the factors powers of two: every step is exact in fp32, so the
-// choice does not depend on the order of the sums, and ties go to the lowest index.
+// are whole numbers below 2^21 and the factors powers of two: every step is exact in fp32 (within its
+// normal range), so the choice does not depend on the order of the sums, and ties go to the lowest index.
 //
 // The scores are a product of the bounds (16 blocks a warp) with the rows (8 at a time) on the
 // integer tensor path, mma.sync m16n8k32: the bytes go from memory to operands as they are.  A
@@ -18,7 +18,8 @@
 //
 // Measured (B200, d = 128): 128 of up to 1024 blocks for 32 sequences of 8 KV heads, 42 MB of bounds,
 // 20 us, of which the choice is 6 (it is serial: its barriers and loads wait with little else in
-// flight); 64 of 2048 blocks for one sequence 8 us, the choice 4.  Eviction of half of the blocks of
+// flight); 64 of 2048 blocks for one sequence 9 us, the choice 4; 128 of 8192 23 us, of 10240 through
+// the second kernel 25.  Eviction of half of the blocks of
 // 32 layers x 2 sequences x 8 heads, 262 MB of codes in and out, 93 us = 5.9 TB/s; of one layer of 4
 // sequences 8.5 us, latency.
 #include <cooperative_groups.h>
